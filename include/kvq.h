@@ -50,7 +50,8 @@ typedef enum kvq_status {
   KVQ_ERR_WORKSPACE = 4,    /* workspace missing or smaller than kvq_decode_plan says */
   KVQ_ERR_CUDA = 5,         /* a CUDA launch or query failed */
   KVQ_ERR_BAD_INDEX = 6,    /* device saw a slot / block id outside the cache */
-  KVQ_ERR_TIMEOUT = 7       /* a bounded device wait gave up */
+  KVQ_ERR_TIMEOUT = 7,      /* a bounded device wait gave up */
+  KVQ_ERR_NO_BLOCKS = 8     /* device found fewer free blocks than a call asked for */
 } kvq_status;
 
 /* Cache dtype and scale layout of one layer ([P1] "Per-tensor vs per-head FP8
@@ -161,6 +162,185 @@ kvq_status kvq_cache_write(const kvq_ctx* ctx, int layer, const void* k_new, con
  * scale_out: device fp32 [Hkv], overwritten. */
 kvq_status kvq_calibrate_per_head(const kvq_ctx* ctx, const void* x, long long num_tokens,
                                   float qmax, float* scale_out, void* stream);
+
+/* ------------------------------------------------------------- rotary positions
+ * Pair i (0 <= i < rotary_dim / 2) of a head vector x at position p becomes
+ *   x'[a] = m (x[a] cos(p f_i) - x[b] sin(p f_i))
+ *   x'[b] = m (x[a] sin(p f_i) + x[b] cos(p f_i))
+ * with (a, b) = (i, i + rotary_dim/2) (KVQ_ROPE_HALF) or (2i, 2i + 1)
+ * (KVQ_ROPE_INTERLEAVED), and elements from rotary_dim on pass through.  The
+ * pages have no counterpart; q and k reach kvq_cache_write and the attention
+ * calls rotated, and these calls are how they get there. */
+typedef enum kvq_rope_layout { KVQ_ROPE_HALF = 0, KVQ_ROPE_INTERLEAVED = 1 } kvq_rope_layout;
+
+/* How the frequencies f_i = base^(-2i / rotary_dim) are scaled for contexts
+ * longer than the model was trained on, s = factor:
+ *  KVQ_ROPE_PLAIN   not at all
+ *  KVQ_ROPE_LINEAR  f_i / s (positions interpolated)
+ *  KVQ_ROPE_BASE    base replaced by base s^(r / (r - 2)), r = rotary_dim
+ *  KVQ_ROPE_PARTS   by the turns n_i = original_context f_i / (2 pi) that pair
+ *                   i makes over the original context: kept above
+ *                   high_rotations, f_i / s below low_rotations, and
+ *                   g f_i + (1 - g) f_i / s with g = (n_i - low) / (high - low)
+ *                   between. */
+typedef enum kvq_rope_scaling {
+  KVQ_ROPE_PLAIN = 0,
+  KVQ_ROPE_LINEAR = 1,
+  KVQ_ROPE_BASE = 2,
+  KVQ_ROPE_PARTS = 3
+} kvq_rope_scaling;
+
+typedef struct kvq_rope_config {
+  int head_dim;               /* 64, 128 or 256 */
+  int rotary_dim;             /* a multiple of 16, 16..head_dim */
+  int layout;                 /* kvq_rope_layout */
+  int scaling;                /* kvq_rope_scaling */
+  double base;                /* > 0 */
+  double factor;              /* > 0; read by the scaled kinds only */
+  double original_context;    /* > 0; KVQ_ROPE_PARTS only */
+  double low_rotations;       /* KVQ_ROPE_PARTS only, 0 <= low < high */
+  double high_rotations;
+  float magnitude;            /* m above, 1/16..16; 0 => 1 */
+  const double* frequencies;  /* host [rotary_dim / 2], copied: the f_i themselves (scaling must
+                                 be KVQ_ROPE_PLAIN, base is not read); NULL = from base */
+} kvq_rope_config;
+
+typedef struct kvq_rope kvq_rope;
+
+/* Validates *cfg and computes the frequencies into a new handle.  Host only;
+ * no CUDA call and no device memory.  KVQ_ERR_INVALID_ARG for a null pointer, a
+ * value outside the ranges above or not finite, KVQ_ERR_UNSUPPORTED for a
+ * head_dim or rotary_dim that is not built.  *out is NULL on error; the caller
+ * releases a handle with kvq_rope_destroy.  A handle may be shared by threads. */
+kvq_status kvq_rope_create(const kvq_rope_config* cfg, kvq_rope** out);
+void kvq_rope_destroy(kvq_rope* rope);
+
+/* The frequencies f_i after scaling (host double [rotary_dim / 2]) and m. */
+kvq_status kvq_rope_frequencies(const kvq_rope* rope, double* frequencies, float* magnitude);
+
+/* Rotation alone: out[t][h] = the rotation of x[t][h] at positions[t].
+ * x, out: bf16 [num_tokens][num_heads][head_dim], token t starting at element
+ *   t * its stride (0 => num_heads * head_dim); 16-byte aligned, strides
+ *   multiples of 8 and at least num_heads * head_dim.  out may be x (with the
+ *   same stride); otherwise they must not overlap.
+ * positions: int64 [num_tokens], any value (negative ones included).
+ * inverse: nonzero turns by -p f_i, still times m.  That is the transpose of the
+ *   map, hence its gradient with respect to x, and for m = 1 its inverse.
+ * Angles are taken modulo one turn in 64-bit fixed point, so far positions are
+ * as exact as near ones; the rotation is computed in fp32 and rounded to bf16
+ * once. */
+kvq_status kvq_rope_apply(const kvq_rope* rope, const void* x, long long x_token_stride,
+                          const long long* positions, long long num_tokens, int num_heads,
+                          void* out, long long out_token_stride, int inverse, void* stream);
+
+/* kvq_cache_write of rotated keys, with the queries rotated in the same launch.
+ *
+ * q, q_out: bf16 [num_tokens][Hq][D] with token strides as for kvq_rope_apply
+ *   (0 => Hq*D); q_out gets the rotated queries of EVERY token (bf16, what the
+ *   attention calls take) and may be q.  Both NULL: no queries.
+ * k_new, v_new, kv_token_stride, slot_mapping, scales and caches as for
+ *   kvq_cache_write.  k is rotated at positions[t] in fp32 and quantized from
+ *   there, without the rounding to bf16 that a rotation followed by
+ *   kvq_cache_write has in between (a BF16 layer rounds once, to the same bits);
+ *   v is stored as kvq_cache_write stores it.  q, k and v may be parts of one
+ *   fused buffer.  A token with slot < 0 has its q rotated and stores nothing.
+ * Two tokens with the same slot leave one of the two there, as in
+ * kvq_cache_write. */
+kvq_status kvq_rope_cache_write(const kvq_ctx* ctx, const kvq_rope* rope, int layer, const void* q,
+                                long long q_token_stride, void* q_out,
+                                long long q_out_token_stride, const void* k_new,
+                                const void* v_new, long long kv_token_stride,
+                                const long long* positions, const long long* slot_mapping,
+                                long long num_tokens, const float* k_scale, const float* v_scale,
+                                void* k_cache, void* v_cache, float* k_cache_scale,
+                                float* v_cache_scale, void* stream);
+
+/* ------------------------------------------------------------- pages of the pool
+ * One pool of num_blocks blocks serves every layer of a context: a block id
+ * names the same block in each layer's cache.  Its state is three device arrays
+ * of the caller, which every call below reads and updates on the stream:
+ *   ref_count     int32 [num_blocks]   table entries that hold the block; 0 = free
+ *   block_table   int32 [table_rows][max_blocks_per_seq]   as the attention calls take it
+ *   context_lens  int32 [table_rows]   positions of the row; ceil(len / block_size)
+ *                                      entries of its table row are in use
+ * An empty pool is ref_count 0, context_lens 0 and any table.  The calls keep
+ *   ref_count[b] = the number of used table entries that hold b.
+ * They need no workspace, allocate nothing, never synchronise and can be
+ * captured into a graph; calls on one pool must be ordered by the caller (one
+ * stream, or events).  Rows whose entries repeat a block (rings of window
+ * layers) are not for these calls.
+ *
+ * A row index outside the table, a row that a call may name once and names
+ * again, a length that is negative or past the row's entries, and a block id
+ * outside the pool set KVQ_ERR_BAD_INDEX on the device word; that row (that
+ * entry, for a block id) is left as it is and the others proceed.  num_rows or
+ * num_forks = 0 is KVQ_OK. */
+
+/* Takes num_rows rows and new_tokens[i] >= 0 further positions for row rows[i]
+ * (distinct rows): hands out the blocks they need, lowest free ids first in the
+ * order of the rows, and gives what the write and the prefill take.
+ *   query_start   int32 [num_rows + 1]  prefix sums of new_tokens
+ *   positions     int64 [max_tokens]    position of each new token
+ *   slot_mapping  int64 [max_tokens]    its slot; -1 for a token of a refused row
+ *   copies        int32 [num_rows][2]   see below
+ * Entries from query_start[num_rows] to max_tokens are filled with position 0
+ * and slot -1 (a padded batch).
+ * A row whose last block is partly filled and held by another entry too gets a
+ * block of its own for it: copies[i] = (shared block, new block), which
+ * kvq_copy_blocks must copy before anything is written; else (-1, -1).
+ * A row gets all that it asks for or nothing.  When the rows up to and including
+ * row i need more blocks than are free, row i is refused if it needs any
+ * (KVQ_ERR_NO_BLOCKS on the device word); when they have more than max_tokens
+ * tokens it is refused too (KVQ_ERR_BAD_INDEX).  A refused row keeps its length
+ * and table.  num_rows <= 4096; max_tokens < 2^31. */
+kvq_status kvq_extend_sequences(const kvq_ctx* ctx, const int* rows, const int* new_tokens,
+                                int num_rows, int* ref_count, int* block_table, int table_rows,
+                                int max_blocks_per_seq, int* context_lens, long long max_tokens,
+                                int* query_start, long long* positions, long long* slot_mapping,
+                                int* copies, void* stream);
+
+/* Row children[i] becomes a copy of row parents[i] that shares all its blocks
+ * (no page is copied until one of them grows; see kvq_extend_sequences).
+ * Children are distinct, empty rows (length 0); a parent may be named often, but
+ * not as a child of the same call. */
+kvq_status kvq_fork_sequences(const kvq_ctx* ctx, const int* parents, const int* children,
+                              int num_forks, int* ref_count, int* block_table, int table_rows,
+                              int max_blocks_per_seq, int* context_lens, void* stream);
+
+/* Cuts row rows[i] (distinct rows) to its first min(length, keep_lens[i])
+ * positions, or to none with keep_lens NULL: blocks past them lose a holder (and
+ * are free when it was the last), their table entries become -1. */
+kvq_status kvq_truncate_sequences(const kvq_ctx* ctx, const int* rows, const int* keep_lens,
+                                  int num_rows, int* ref_count, int* block_table, int table_rows,
+                                  int max_blocks_per_seq, int* context_lens, void* stream);
+
+/* Renames blocks so that those in use become 0 .. n-1, n their number: block
+ * ids >= n in use go to the free ids below n, both in ascending order.  Tables
+ * and reference counts are rewritten.
+ *   moves      int32 [num_blocks / 2][2]  (old, new) id of each block that moved
+ *   num_moves  int32 [1]                  their number; later entries are not written
+ * kvq_copy_blocks(moves, num_blocks / 2, num_moves) then moves the pages of
+ * every layer, before they are read or written. */
+kvq_status kvq_compact_blocks(const kvq_ctx* ctx, int* ref_count, int* block_table,
+                              int table_rows, int max_blocks_per_seq, int* context_lens,
+                              int* moves, int* num_moves, void* stream);
+
+/* Copies block pairs[i][0] to block pairs[i][1] in the caches of num_layers
+ * layers from first_layer on: K and V codes and, for dynamic modes, scales.
+ *   pairs      device int32 [max_pairs][2]; a negative source is skipped, an id
+ *              outside the pool is skipped and sets KVQ_ERR_BAD_INDEX
+ *   num_pairs  device int32 [1]: the first min(*num_pairs, max_pairs) pairs are
+ *              copied; NULL = max_pairs
+ *   k_caches, v_caches, k_cache_scales, v_cache_scales: HOST arrays [num_layers]
+ *              of the layers' device buffers (16-byte aligned; read during the
+ *              call); the scale arrays may be NULL when no layer is dynamic, and
+ *              entries of other layers are not read
+ * The pairs are copied at once: destinations are distinct and none is another
+ * pair's source (the pairs that the calls above give are so). */
+kvq_status kvq_copy_blocks(const kvq_ctx* ctx, int first_layer, int num_layers, const int* pairs,
+                           int max_pairs, const int* num_pairs, void* const* k_caches,
+                           void* const* v_caches, float* const* k_cache_scales,
+                           float* const* v_cache_scales, void* stream);
 
 /* Work plan for a decode call.  The retained positions of all (sequence, KV
  * head) items are cut into 16-position tiles and divided evenly among
@@ -334,7 +514,8 @@ kvq_status kvq_decode_attention_fixed_scratch(const kvq_ctx* ctx, int layer, con
 kvq_status kvq_e4m3_encode(const float* in, unsigned char* out, long long n, void* stream);
 
 /* Synchronizes `stream`, returns the device error word of the current device
- * as a status (KVQ_OK, KVQ_ERR_BAD_INDEX or KVQ_ERR_TIMEOUT) and clears it. */
+ * as a status (KVQ_OK, KVQ_ERR_BAD_INDEX, KVQ_ERR_TIMEOUT or
+ * KVQ_ERR_NO_BLOCKS) and clears it. */
 kvq_status kvq_get_device_error(void* stream);
 
 /* Check of the timeout path (no counterpart on the pages).  Every wait of the

@@ -7,17 +7,9 @@
 
 #include <mutex>
 #include <new>
-#include <vector>
-
+#include "api_common.h"
 #include "kvq.h"
 #include "kvq_internal.h"
-
-struct kvq_ctx {
-  kvq_config cfg;
-  std::vector<int> mode;
-  std::vector<int> window;
-  float softmax_scale;
-};
 
 namespace kvq {
 
@@ -36,30 +28,9 @@ int sm_count() {
 
 }  // namespace kvq
 
+using namespace kvq;
+
 namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-bool is_dynamic(int mode) {
-  return mode == KVQ_FP8_PER_TOKEN_HEAD || mode == KVQ_INT4_PER_TOKEN_HEAD;
-}
-
-double elem_bytes(int mode) {
-  return mode == KVQ_BF16 ? 2.0 : (mode == KVQ_INT4_PER_TOKEN_HEAD ? 0.5 : 1.0);
-}
-
-long long row_bytes(int mode, int D) {
-  return mode == KVQ_BF16 ? 2LL * D : (mode == KVQ_INT4_PER_TOKEN_HEAD ? D / 2 : D);
-}
-
-kvq_status check_layer(const kvq_ctx* ctx, int layer) {
-  if (!ctx) return KVQ_ERR_INVALID_ARG;
-  if (layer < 0 || layer >= ctx->cfg.num_layers) return KVQ_ERR_INVALID_ARG;
-  return KVQ_OK;
-}
-
-kvq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
 // Worker warps for a decode call: enough to fill every SM at the kernel's
 // occupancy, but no more than one per 4 tiles (64 positions) of work, so a
@@ -480,6 +451,7 @@ kvq_status kvq_get_device_error(void* stream) {
   }
   if (v & kvq::ERR_TIMEOUT) return KVQ_ERR_TIMEOUT;
   if (v & kvq::ERR_BAD_INDEX) return KVQ_ERR_BAD_INDEX;
+  if (v & kvq::ERR_NO_BLOCKS) return KVQ_ERR_NO_BLOCKS;
   return KVQ_OK;
 }
 
@@ -561,6 +533,7 @@ const char* kvq_status_string(kvq_status s) {
     case KVQ_ERR_CUDA: return "CUDA error";
     case KVQ_ERR_BAD_INDEX: return "slot or block id outside the cache";
     case KVQ_ERR_TIMEOUT: return "device wait timed out";
+    case KVQ_ERR_NO_BLOCKS: return "too few free blocks in the pool";
   }
   return "unknown status";
 }

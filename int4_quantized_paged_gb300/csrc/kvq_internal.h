@@ -12,7 +12,7 @@ enum Mode { BF16 = 0, FP8_PER_TENSOR = 1, FP8_PER_HEAD = 2, FP8_PER_TOKEN_HEAD =
             INT4_PER_TOKEN_HEAD = 4 };
 
 // Device error word bits.
-enum : unsigned { ERR_BAD_INDEX = 1u, ERR_TIMEOUT = 2u };
+enum : unsigned { ERR_BAD_INDEX = 1u, ERR_TIMEOUT = 2u, ERR_NO_BLOCKS = 4u };
 
 struct WriteArgs {
   const uint16_t* k_new;       // bf16 bits
@@ -57,8 +57,75 @@ struct DecodeArgs {
   float qk_scale;              // softmax_scale * log2(e)
 };
 
+enum RopeLayout { ROPE_HALF = 0, ROPE_INTERLEAVED = 1 };
+constexpr int ROPE_MAX_PAIRS = 128;
+
+// Frequencies of a rotation as fractions of a turn per position times 2^64.
+struct RopeTable {
+  unsigned long long phase[ROPE_MAX_PAIRS];
+  float magnitude;
+};
+
+struct RopeArgs {
+  WriteArgs w;                 // k, v, slots, caches (Hkv 0, slots nullptr: rotation only)
+  const uint16_t* q;           // bf16, token stride q_stride (Hq 0: none)
+  uint16_t* q_out;             // may be q
+  long long q_stride, q_out_stride;
+  const long long* positions;  // [T]
+  int Hq;
+  int rotary;                  // rotated elements of a head
+  float sin_magnitude;         // magnitude, negative for the transpose
+  int slices, per_slice;       // set by the launcher: slices of a token's vectors, vectors in each
+};
+
+// Page tables and reference counts of a pool of num_blocks blocks.
+struct PageTables {
+  int* ref;                    // [num_blocks]
+  int* table;                  // [rows][max_blocks]
+  int* lens;                   // [rows]
+  long long num_blocks;
+  int rows, max_blocks, bs, bs_shift;
+  unsigned* err;
+};
+
+struct ExtendArgs {
+  const int* rows;             // [n]
+  const int* new_tokens;       // [n]
+  int n;
+  long long max_tokens;
+  int* query_start;            // [n + 1]
+  long long* positions;        // [max_tokens]
+  long long* slots;            // [max_tokens]
+  int* copies;                 // [n][2]
+};
+constexpr int EXTEND_MAX_ROWS = 4096;
+
+struct CopyLayer {
+  void* buf[4];                // K codes, V codes, K scales, V scales
+  unsigned code_chunks, scale_chunks;   // 16-byte chunks of one block in a code / scale buffer
+};
+constexpr int COPY_MAX_LAYERS = 80;     // per launch (the kernel's parameters end at 4 KB)
+
+struct CopyArgs {
+  CopyLayer layer[COPY_MAX_LAYERS];
+  const int* pairs;            // [max_pairs][2]
+  const int* num_pairs;        // device count, or nullptr
+  int max_pairs, layers;
+  long long num_blocks;
+  unsigned* err;
+};
+
 // Launchers (return cudaGetLastError() of the launch).
 cudaError_t launch_cache_write(int mode, int D, const WriteArgs& a, cudaStream_t st);
+cudaError_t launch_rope(int mode, int D, int layout, RopeArgs a, const RopeTable& tab,
+                        cudaStream_t st);
+cudaError_t launch_truncate(const PageTables& t, const int* rows, const int* keep_lens, int n,
+                            cudaStream_t st);
+cudaError_t launch_fork(const PageTables& t, const int* parents, const int* children, int n,
+                        cudaStream_t st);
+cudaError_t launch_extend(const PageTables& t, const ExtendArgs& x, cudaStream_t st);
+cudaError_t launch_compact(const PageTables& t, int* moves, int* num_moves, cudaStream_t st);
+cudaError_t launch_copy_blocks(const CopyArgs& a, cudaStream_t st);
 cudaError_t launch_calibrate(const uint16_t* x, long long T, int Hkv, int D, float qmax,
                              float* out, cudaStream_t st);
 cudaError_t launch_e4m3_encode(const float* in, uint8_t* out, long long n, cudaStream_t st);

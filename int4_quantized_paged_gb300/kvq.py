@@ -26,9 +26,13 @@ MODE_NAMES = {"bf16": BF16, "fp8_per_tensor": FP8_PER_TENSOR, "fp8_per_head": FP
               "fp8_per_token_head": FP8_PER_TOKEN_HEAD, "int4_per_token_head": INT4_PER_TOKEN_HEAD}
 DYNAMIC = (FP8_PER_TOKEN_HEAD, INT4_PER_TOKEN_HEAD)
 STATUS = ["KVQ_OK", "KVQ_ERR_INVALID_ARG", "KVQ_ERR_UNSUPPORTED", "KVQ_ERR_ALIGNMENT",
-          "KVQ_ERR_WORKSPACE", "KVQ_ERR_CUDA", "KVQ_ERR_BAD_INDEX", "KVQ_ERR_TIMEOUT"]
+          "KVQ_ERR_WORKSPACE", "KVQ_ERR_CUDA", "KVQ_ERR_BAD_INDEX", "KVQ_ERR_TIMEOUT",
+          "KVQ_ERR_NO_BLOCKS"]
+ROPE_HALF, ROPE_INTERLEAVED = range(2)
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS = range(4)
 
 P, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
+f64 = ctypes.c_double
 
 
 class kvq_config(ctypes.Structure):
@@ -46,12 +50,29 @@ class kvq_capacity(ctypes.Structure):
                 ("cache_bytes", ctypes.c_double), ("bf16_cache_bytes", ctypes.c_double)]
 
 
+class kvq_rope_config(ctypes.Structure):
+    _fields_ = [("head_dim", i32), ("rotary_dim", i32), ("layout", i32), ("scaling", i32),
+                ("base", f64), ("factor", f64), ("original_context", f64), ("low_rotations", f64),
+                ("high_rotations", f64), ("magnitude", f32), ("frequencies", ctypes.POINTER(f64))]
+
+
 _SIGS = {
     "kvq_create": (i32, [ctypes.POINTER(kvq_config), ctypes.POINTER(P)]),
     "kvq_destroy": (None, [P]),
     "kvq_layer_buffer_sizes": (i32, [P, i32, ctypes.POINTER(sz), ctypes.POINTER(sz)]),
     "kvq_cache_bytes": (i32, [P, i64, ctypes.POINTER(kvq_capacity)]),
     "kvq_cache_write": (i32, [P, i32, P, P, i64, P, i64, P, P, P, P, P, P, P]),
+    "kvq_rope_create": (i32, [ctypes.POINTER(kvq_rope_config), ctypes.POINTER(P)]),
+    "kvq_rope_destroy": (None, [P]),
+    "kvq_rope_frequencies": (i32, [P, ctypes.POINTER(f64), ctypes.POINTER(f32)]),
+    "kvq_rope_apply": (i32, [P, P, i64, P, i64, i32, P, i64, i32, P]),
+    "kvq_rope_cache_write": (i32, [P, P, i32, P, i64, P, i64, P, P, i64, P, P, i64, P, P, P, P, P,
+                                   P, P]),
+    "kvq_extend_sequences": (i32, [P, P, P, i32, P, P, i32, i32, P, i64, P, P, P, P, P]),
+    "kvq_fork_sequences": (i32, [P, P, P, i32, P, P, i32, i32, P, P]),
+    "kvq_truncate_sequences": (i32, [P, P, P, i32, P, P, i32, i32, P, P]),
+    "kvq_compact_blocks": (i32, [P, P, P, i32, i32, P, P, P, P]),
+    "kvq_copy_blocks": (i32, [P, i32, i32, P, i32, P, P, P, P, P, P]),
     "kvq_calibrate_per_head": (i32, [P, P, i64, f32, P, P]),
     "kvq_decode_plan": (i32, [P, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(sz)]),
     "kvq_decode_workspace_size": (sz, [P, i32, i32, i32]),
@@ -177,6 +198,135 @@ def kvq_cache_write(ctx: Context, layer: int, k_new, v_new, slot_mapping, k_cach
                                 _ptr(slot_mapping), T, _ptr(k_scale), _ptr(v_scale),
                                 _ptr(k_cache), _ptr(v_cache), _ptr(k_cache_scale),
                                 _ptr(v_cache_scale), _stream(stream)), "kvq_cache_write")
+
+
+class Rope:
+    """Owns a kvq_rope handle (host-only: frequencies and layout)."""
+
+    def __init__(self, handle: int, cfg: dict):
+        self.handle = handle
+        self.cfg = cfg
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h:
+            _lib.kvq_rope_destroy(h)
+
+    @property
+    def _as_parameter_(self):
+        return ctypes.c_void_p(self.handle)
+
+
+def kvq_rope_create(head_dim: int, rotary_dim: Optional[int] = None, *, layout: int = ROPE_HALF,
+                    base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+                    original_context: float = 0.0, low_rotations: float = 0.0,
+                    high_rotations: float = 0.0, magnitude: float = 1.0,
+                    frequencies: Optional[Sequence[float]] = None) -> Rope:
+    r = head_dim if rotary_dim is None else rotary_dim
+    if frequencies is not None and len(frequencies) < r // 2:
+        raise ValueError("frequencies: rotary_dim / 2 values")
+    fs = None if frequencies is None else (f64 * len(frequencies))(*frequencies)
+    cfg = kvq_rope_config(head_dim, r, layout, scaling, base, factor, original_context,
+                          low_rotations, high_rotations, magnitude,
+                          None if fs is None else ctypes.cast(fs, ctypes.POINTER(f64)))
+    h = P()
+    _check(_lib.kvq_rope_create(ctypes.byref(cfg), ctypes.byref(h)), "kvq_rope_create")
+    return Rope(h.value, dict(head_dim=head_dim, rotary_dim=r, layout=layout))
+
+
+def kvq_rope_frequencies(rope: Rope):
+    """(frequencies after scaling, magnitude)."""
+    fs, m = (f64 * (rope.cfg["rotary_dim"] // 2))(), f32()
+    _check(_lib.kvq_rope_frequencies(rope, fs, ctypes.byref(m)), "kvq_rope_frequencies")
+    return list(fs), m.value
+
+
+def kvq_rope_apply(rope: Rope, x, positions, out, *, inverse: bool = False, x_token_stride: int = 0,
+                   out_token_stride: int = 0, num_tokens: Optional[int] = None,
+                   num_heads: Optional[int] = None, stream=None):
+    T = x.shape[0] if num_tokens is None else num_tokens
+    H = x.shape[1] if num_heads is None else num_heads
+    _check(_lib.kvq_rope_apply(rope, _ptr(x), x_token_stride, _ptr(positions), T, H, _ptr(out),
+                               out_token_stride, int(inverse), _stream(stream)), "kvq_rope_apply")
+
+
+def kvq_rope_cache_write(ctx: Context, rope: Rope, layer: int, q, q_out, k_new, v_new, positions,
+                         slot_mapping, k_cache, v_cache, k_cache_scale=None, v_cache_scale=None,
+                         k_scale=None, v_scale=None, q_token_stride: int = 0,
+                         q_out_token_stride: int = 0, kv_token_stride: int = 0,
+                         num_tokens: Optional[int] = None, stream=None):
+    """kvq_cache_write of rotated keys; rotates q into q_out too (both None: keys only)."""
+    T = k_new.shape[0] if num_tokens is None else num_tokens
+    _check(_lib.kvq_rope_cache_write(
+        ctx, rope, layer, _ptr(q), q_token_stride, _ptr(q_out), q_out_token_stride, _ptr(k_new),
+        _ptr(v_new), kv_token_stride, _ptr(positions), _ptr(slot_mapping), T, _ptr(k_scale),
+        _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), _ptr(k_cache_scale), _ptr(v_cache_scale),
+        _stream(stream)), "kvq_rope_cache_write")
+
+
+def kvq_extend_sequences(ctx: Context, rows, new_tokens, ref_count, block_table, context_lens,
+                         query_start, positions, slot_mapping, copies, *,
+                         max_tokens: Optional[int] = None, stream=None):
+    """Blocks, positions and slots for new_tokens[i] more tokens of row rows[i]."""
+    n = positions.numel() if max_tokens is None else max_tokens
+    _check(_lib.kvq_extend_sequences(
+        ctx, _ptr(rows), _ptr(new_tokens), rows.numel(), _ptr(ref_count), _ptr(block_table),
+        block_table.shape[0], block_table.shape[1], _ptr(context_lens), n, _ptr(query_start),
+        _ptr(positions), _ptr(slot_mapping), _ptr(copies), _stream(stream)), "kvq_extend_sequences")
+
+
+def kvq_fork_sequences(ctx: Context, parents, children, ref_count, block_table, context_lens,
+                       stream=None):
+    _check(_lib.kvq_fork_sequences(ctx, _ptr(parents), _ptr(children), parents.numel(),
+                                   _ptr(ref_count), _ptr(block_table), block_table.shape[0],
+                                   block_table.shape[1], _ptr(context_lens), _stream(stream)),
+           "kvq_fork_sequences")
+
+
+def kvq_truncate_sequences(ctx: Context, rows, keep_lens, ref_count, block_table, context_lens,
+                           stream=None):
+    """keep_lens None frees the rows."""
+    _check(_lib.kvq_truncate_sequences(ctx, _ptr(rows), _ptr(keep_lens), rows.numel(),
+                                       _ptr(ref_count), _ptr(block_table), block_table.shape[0],
+                                       block_table.shape[1], _ptr(context_lens), _stream(stream)),
+           "kvq_truncate_sequences")
+
+
+def kvq_compact_blocks(ctx: Context, ref_count, block_table, context_lens, moves, num_moves,
+                       stream=None):
+    """moves: int32 [num_blocks // 2, 2] (old, new); num_moves: int32 [1]."""
+    _check(_lib.kvq_compact_blocks(ctx, _ptr(ref_count), _ptr(block_table), block_table.shape[0],
+                                   block_table.shape[1], _ptr(context_lens), _ptr(moves),
+                                   _ptr(num_moves), _stream(stream)), "kvq_compact_blocks")
+
+
+class LayerPointers:
+    """Host arrays of the layers' cache pointers that kvq_copy_blocks takes; made
+    once for the caches of a program, whose tensors it keeps alive."""
+
+    def __init__(self, k_caches, v_caches, k_cache_scales=None, v_cache_scales=None):
+        groups = [list(k_caches), list(v_caches), list(k_cache_scales or []),
+                  list(v_cache_scales or [])]
+        self.tensors = groups
+        self.num_layers = len(groups[0])
+        self.arrays = [(P * len(g))(*[_ptr(t) for t in g]) if g else None for g in groups]
+
+
+def layer_pointers(k_caches, v_caches, k_cache_scales=None, v_cache_scales=None) -> LayerPointers:
+    """Pointers of every layer's buffers (entries of the scale lists may be None)."""
+    lists = [x for x in (k_caches, v_caches, k_cache_scales, v_cache_scales) if x is not None]
+    if len({len(x) for x in lists}) != 1:
+        raise ValueError("one buffer of each kind for every layer")
+    return LayerPointers(k_caches, v_caches, k_cache_scales, v_cache_scales)
+
+
+def kvq_copy_blocks(ctx: Context, pairs, layers: LayerPointers, *, num_pairs=None,
+                    first_layer: int = 0, max_pairs: Optional[int] = None, stream=None):
+    """Copies block pairs[i, 0] to pairs[i, 1] in every layer of `layers`."""
+    n = pairs.shape[0] if max_pairs is None else max_pairs
+    _check(_lib.kvq_copy_blocks(ctx, first_layer, layers.num_layers, _ptr(pairs), n,
+                                _ptr(num_pairs), *layers.arrays, _stream(stream)),
+           "kvq_copy_blocks")
 
 
 def kvq_calibrate_per_head(ctx: Context, x, scale_out, qmax: float = 448.0,
