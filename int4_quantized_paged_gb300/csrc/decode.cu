@@ -812,10 +812,13 @@ __global__ void __launch_bounds__(WARPS * 32, MinCtas<MODE, D, G>::value)
         kq[0] = k0 * sq[0]; kq[1] = k0 * sq[1]; kq[2] = k1 * sq[0]; kq[3] = k1 * sq[1];
         vs0 = ksc[16 + lg];
         vs1 = ksc[16 + lg + 8];
-        // rows outside [lo, L) may hold anything: only retained rows count
+        // rows outside [lo, L) may hold anything, NaN too: only retained rows
+        // count, and the others' weight 0 meets a scale of 0
         const int p0 = pos0 + lg, p1 = p0 + 8;
-        vraise = ((whole || (p0 >= lo && p0 < L)) && vs0 >= vcap) ||
-                 ((whole || (p1 >= lo && p1 < L)) && vs1 >= vcap);
+        const bool in0 = whole || (p0 >= lo && p0 < L), in1 = whole || (p1 >= lo && p1 < L);
+        vraise = (in0 && vs0 >= vcap) || (in1 && vs1 >= vcap);
+        if (!in0) vs0 = 0.f;
+        if (!in1) vs1 = 0.f;
       }
     }
     float s_raw[4];
