@@ -475,6 +475,51 @@ kvq_status kvq_prefill_attention(const kvq_ctx* ctx, int layer, const void* q,
                                  const int* context_lens, int batch, int max_query_len,
                                  float* out, void* stream);
 
+/* Cross attention: the queries of each sequence attend to ALL positions of an
+ * encoder's states, which are in the paged cache (written by kvq_cache_write; a
+ * cache of this kind is usually a context of its own, filled once per request
+ * and shared by its beams through their table rows).  Without a mask and
+ * without rotated positions, of another length than the queries:
+ *   out[t] = sum_p softmax(softmax_scale <q[t], K_hat[p]>) V_hat[p],
+ *   p in [0, encoder_lens[b]).
+ * The pages have no counterpart; K_hat, V_hat and the scale layouts are those
+ * of kvq_decode_attention.
+ *
+ * q: bf16 [T][Hq][D]; out: bf16 [T][Hq][D], both 16-byte aligned.
+ * query_start: int32 [batch + 1] as for kvq_prefill_attention: sequence b has
+ *   rows [query_start[b], query_start[b + 1]), none included.  NULL: one query
+ *   per sequence, row b (a decoding step); max_query_len is then 0 or 1.
+ * encoder_lens: int32 [batch].  0 gives zero rows.
+ * max_query_len: an upper bound of the queries of a sequence; rows past it set
+ *   KVQ_ERR_BAD_INDEX on the device word and are not computed.
+ * max_encoder_len: an upper bound of encoder_lens, used by the plan only; more
+ *   than the table rows cover is KVQ_ERR_INVALID_ARG.
+ * num_splits, workspace: from kvq_cross_plan with the same sizes; num_splits 0
+ *   = the plan's choice.  The workspace (16-byte aligned) needs no
+ *   initialisation; overlapping calls need one each.
+ * Softmax and sums are fp32; the weight that meets a value is rounded to f16
+ * (an eighth of the output's own rounding).  A layer with a window is
+ * KVQ_ERR_UNSUPPORTED.  A length that is negative or past the table row sets
+ * KVQ_ERR_BAD_INDEX and leaves that sequence's rows as they were (with
+ * query_start NULL: as kvq_decode_attention treats it); a block id outside the
+ * cache sets it and leaves the page's positions out.  Scale pointers as for
+ * kvq_decode_attention; dynamic scale buffers are 16-byte aligned. */
+kvq_status kvq_cross_attention(const kvq_ctx* ctx, int layer, const void* q, const void* k_cache,
+                               const void* v_cache, const float* k_scale, const float* v_scale,
+                               const float* k_cache_scale, const float* v_cache_scale,
+                               const int* block_table, int max_blocks_per_seq,
+                               const int* query_start, const int* encoder_lens, int batch,
+                               int max_query_len, int max_encoder_len, void* out, int num_splits,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Splits of the keys and workspace bytes of a kvq_cross_attention call: on input
+ * *num_splits > 0 (at most 1024) requests a count, 0 asks for the plan's choice
+ * (one split when the queries fill the SMs; for few queries, as many as do).
+ * max_query_len 0 plans the form with query_start NULL (*num_splits then counts
+ * worker warps, as in kvq_decode_plan). */
+kvq_status kvq_cross_plan(const kvq_ctx* ctx, int layer, int batch, int max_query_len,
+                          int max_encoder_len, int* num_splits, size_t* workspace_bytes);
+
 /* Decode attention that allocates nothing and needs no workspace from the
  * caller.  The pages have no counterpart to this call; it exists for callers
  * that cannot provide device scratch: code running where no device allocator

@@ -1,5 +1,6 @@
-// C ABI of the operators around the cache: rotary positions and the pages of the
-// pool.  Argument validation and dispatch; everything here runs on the host.
+// C ABI of the operators around the cache: rotary positions, the pages of the
+// pool and cross attention.  Argument validation, the split plan and dispatch;
+// everything here runs on the host.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -60,6 +61,28 @@ kvq_status check_tables(const kvq_ctx* ctx, const int* ref_count, const int* blo
   if (!aligned4(ref_count) || !aligned4(block_table) || !aligned4(context_lens))
     return KVQ_ERR_ALIGNMENT;
   return KVQ_OK;
+}
+
+// Splits of the keys for `base` CTAs (query tiles x sequences x KV heads) over
+// `tiles` key tiles: the count whose waves over the SMs take the least time, in
+// units of a key tile (about 1 us): a CTA costs its tiles and about three more
+// for its queries, barriers and epilogue; joining splits costs about three and
+// a little per split.
+int plan_splits(long long base, int tiles) {
+  const int sms = sm_count();
+  int best = 1;
+  double best_cost = 1e300;
+  for (int s = 1; s <= tiles && s <= 128; ++s) {
+    const int per = (tiles + s - 1) / s;
+    if (s > 1 && (tiles + per - 1) / per != s) continue;     // fewer splits do the same
+    const double waves = (double)((base * s + sms - 1) / sms);
+    const double cost = waves * (per + 3.0) + (s > 1 ? 3.0 + 0.05 * s : 0.0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -356,6 +379,106 @@ kvq_status kvq_copy_blocks(const kvq_ctx* ctx, int first_layer, int num_layers, 
     if (st != KVQ_OK) return st;
   }
   return KVQ_OK;
+}
+
+// ---------------------------------------------------------------- cross attention
+kvq_status kvq_cross_plan(const kvq_ctx* ctx, int layer, int batch, int max_query_len,
+                          int max_encoder_len, int* num_splits, size_t* workspace_bytes) {
+  kvq_status st = check_layer(ctx, layer);
+  if (st != KVQ_OK) return st;
+  if (!num_splits || *num_splits < 0 || batch < 0 || max_query_len < 0 || max_encoder_len < 0 ||
+      max_encoder_len > (1 << 30))
+    return KVQ_ERR_INVALID_ARG;
+  if (max_query_len == 0)                       // one query per sequence: the decode's plan
+    return kvq_decode_plan(ctx, layer, batch, max_encoder_len, num_splits, workspace_bytes);
+  const kvq_config& c = ctx->cfg;
+  const int tile = cross_query_tile(c.head_dim, c.num_q_heads / c.num_kv_heads);
+  const long long base = ((long long)max_query_len + tile - 1) / tile * batch * c.num_kv_heads;
+  const int tiles = (int)(((long long)max_encoder_len + CROSS_KEYS - 1) / CROSS_KEYS);
+  if (*num_splits == 0) *num_splits = plan_splits(base, tiles);
+  if (*num_splits > 1024 || base * *num_splits >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
+  if (workspace_bytes)
+    *workspace_bytes = *num_splits <= 1 ? 0
+                                        : (size_t)*num_splits * batch * (size_t)max_query_len *
+                                              c.num_q_heads * (c.head_dim + 1) * sizeof(float);
+  return KVQ_OK;
+}
+
+kvq_status kvq_cross_attention(const kvq_ctx* ctx, int layer, const void* q, const void* k_cache,
+                               const void* v_cache, const float* k_scale, const float* v_scale,
+                               const float* k_cache_scale, const float* v_cache_scale,
+                               const int* block_table, int max_blocks_per_seq,
+                               const int* query_start, const int* encoder_lens, int batch,
+                               int max_query_len, int max_encoder_len, void* out, int num_splits,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  kvq_status st = check_layer(ctx, layer);
+  if (st != KVQ_OK) return st;
+  if (ctx->window[layer] != 0) return KVQ_ERR_UNSUPPORTED;
+  if (batch < 0 || max_query_len < 0 || max_encoder_len < 0 || max_blocks_per_seq < 0 || num_splits < 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (!query_start)
+    return max_query_len > 1
+               ? KVQ_ERR_INVALID_ARG
+               : kvq_decode_attention_bf16(ctx, layer, q, k_cache, v_cache, k_scale, v_scale,
+                                           k_cache_scale, v_cache_scale, block_table,
+                                           max_blocks_per_seq, encoder_lens, batch,
+                                           max_encoder_len, out, num_splits, workspace,
+                                           workspace_bytes, stream);
+  if (batch == 0 || max_query_len == 0) return KVQ_OK;
+  const kvq_config& c = ctx->cfg;
+  const int mode = ctx->mode[layer];
+  if ((long long)max_encoder_len > (long long)max_blocks_per_seq * c.block_size)
+    return KVQ_ERR_INVALID_ARG;
+  if (!q || !k_cache || !v_cache || !block_table || !encoder_lens || !out)
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      !aligned4(block_table) || !aligned4(query_start) || !aligned4(encoder_lens))
+    return KVQ_ERR_ALIGNMENT;
+  if ((mode == KVQ_FP8_PER_TENSOR || mode == KVQ_FP8_PER_HEAD) && (!k_scale || !v_scale))
+    return KVQ_ERR_INVALID_ARG;
+  if (is_dynamic(mode)) {
+    if (!k_cache_scale || !v_cache_scale) return KVQ_ERR_INVALID_ARG;
+    // the kernel fetches 16 scales at a time by bulk copies
+    if (!aligned16(k_cache_scale) || !aligned16(v_cache_scale)) return KVQ_ERR_ALIGNMENT;
+  }
+  int splits = num_splits;
+  size_t need = 0;
+  st = kvq_cross_plan(ctx, layer, batch, max_query_len, max_encoder_len, &splits, &need);
+  if (st != KVQ_OK) return st;
+  if (splits > 1 && (!workspace || workspace_bytes < need)) return KVQ_ERR_WORKSPACE;
+  if (splits > 1 && !aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
+  const size_t rows = (size_t)splits * batch * (size_t)max_query_len * c.num_q_heads;
+  if (rows >= (1ull << 31) * 8) return KVQ_ERR_INVALID_ARG;      // the joining kernel's grid
+  unsigned* err = error_word();
+  if (!err) return KVQ_ERR_CUDA;
+  DecodeArgs a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k_cache = static_cast<const uint8_t*>(k_cache);
+  a.v_cache = static_cast<const uint8_t*>(v_cache);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.k_cs = k_cache_scale;
+  a.v_cs = v_cache_scale;
+  a.block_table = block_table;
+  a.context_lens = encoder_lens;
+  a.out_bf16 = static_cast<uint16_t*>(out);
+  if (splits > 1) {
+    a.ws_o = static_cast<float*>(workspace);
+    a.ws_ml = a.ws_o + rows * c.head_dim;
+  }
+  a.err = err;
+  a.B = batch;
+  a.Hq = c.num_q_heads;
+  a.Hkv = c.num_kv_heads;
+  a.bs = c.block_size;
+  a.bs_shift = __builtin_ctz((unsigned)c.block_size);
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = c.num_blocks;
+  a.qk_scale = ctx->softmax_scale * 1.4426950408889634f;
+  const int tiles = (max_encoder_len + CROSS_KEYS - 1) / CROSS_KEYS;
+  const int per = tiles == 0 ? 1 : (tiles + splits - 1) / splits;
+  return cuda_status(launch_cross(mode, c.head_dim, c.num_q_heads / c.num_kv_heads, a, query_start,
+                                  max_query_len, splits, per, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

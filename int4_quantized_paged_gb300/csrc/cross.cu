@@ -1,0 +1,147 @@
+// Cross attention: the queries of each sequence attend to ALL positions of its
+// cached encoder states (another length, no mask), over the quantized paged
+// cache.  out[t] = sum_p softmax_p(scale <q[t], K_hat[p]>) V_hat[p].
+//
+// Kernel.  The warp-specialised tcgen05 kernel of the prefill in its CROSS form
+// (prefill_ws.cuh): 128 rows (queries x heads of one KV head) per query tile, key
+// tiles of 64, with three differences.
+//  * No mask but the sequence's end, so a row's keys are the CTA's keys.
+//  * The keys of a sequence are cut into splits of whole key tiles when the
+//    queries alone do not fill the SMs (few decoder tokens, long encoder
+//    states): each split leaves O / l in fp32 and the log2 of its weights' sum,
+//    and a second kernel joins them.  A split has a fixed number of tiles, so
+//    ragged lengths spread over the SMs and none waits for the longest.
+//  * The output is bf16, and the weight P' that meets V is one f16 term (11
+//    bits: off by 2^-11 of its value at most) where the fp32 prefill splits it in
+//    two.  That is an eighth of the output's own rounding (2^-8), the errors of many
+//    weights average, and the PV product costs one MMA instead of two.
+//
+// What bounds it: 4 D flops per query row and key on the tensor cores for many
+// queries; for few, the pages' bytes, converted by four warps per SM.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "kvq_internal.h"
+#include "prefill_common.cuh"
+#include "prefill_ws.cuh"
+
+namespace kvq {
+namespace {
+
+static_assert(CROSS_KEYS == WKT, "keys per tile");
+
+// Joins the splits of one (query, head) per warp: weights 2^(lse - max).
+// Queries of sequences that one split covers were written by it.
+template <int D>
+__global__ void __launch_bounds__(256) cross_merge_kernel(const PrefillArgs pa) {
+  const DecodeArgs& a = pa.d;
+  constexpr int DL = D / 32;                   // elements per lane, as float2 pairs
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long rows = (long long)a.B * pa.max_query;
+  const int h = (int)(item % a.Hq);
+  const long long r = item / a.Hq;
+  if (r >= rows) return;
+  const int b = (int)(r / pa.max_query), i = (int)(r - (long long)b * pa.max_query);
+  const int q0 = pa.query_start[b], n_b = pa.query_start[b + 1] - q0;
+  const int L = a.context_lens[b];
+  if (i >= n_b || L <= 0 || (long long)L > ((long long)a.max_blocks << a.bs_shift)) return;
+  const int tiles = (L + CROSS_KEYS - 1) / CROSS_KEYS;
+  const int ns = min(pa.splits, (tiles + pa.split_tiles - 1) / pa.split_tiles);
+  if (ns <= 1) return;
+  const long long step = rows * a.Hq;          // partial rows between splits
+  const long long p0 = r * a.Hq + h;
+  float top = -INFINITY;
+  for (int s = lane; s < ns; s += 32) top = fmaxf(top, a.ws_ml[p0 + s * step]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float2 acc[DL / 2];
+#pragma unroll
+  for (int k = 0; k < DL / 2; ++k) acc[k] = make_float2(0.f, 0.f);
+  float sum = 0.f;
+  const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+  for (int s = 0; s < ns; ++s) {
+    const float w = ex2(a.ws_ml[p0 + s * step] - ref);
+    const float2* o = reinterpret_cast<const float2*>(a.ws_o + (p0 + s * step) * D) + lane;
+    sum += w;
+#pragma unroll
+    for (int k = 0; k < DL / 2; ++k) {
+      const float2 v = o[32 * k];
+      acc[k].x = fmaf(w, v.x, acc[k].x);
+      acc[k].y = fmaf(w, v.y, acc[k].y);
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  uint32_t* out = reinterpret_cast<uint32_t*>(a.out_bf16 + ((long long)(q0 + i) * a.Hq + h) * D) + lane;
+#pragma unroll
+  for (int k = 0; k < DL / 2; ++k) out[32 * k] = pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
+}
+
+template <int MODE, int D>
+cudaError_t claunch(const PrefillArgs& pa, cudaStream_t st) {
+  using C = WCfg<MODE, D>;
+  const DecodeArgs& a = pa.d;
+  const long long total = a.num_blocks * a.Hkv * a.bs * (long long)C::RB;
+  CUtensorMap km = {}, vm = {};
+  if (total > 0) {
+    const bool kok = C::KDIRECT ? make_kblock_map(&km, a.k_cache, total, C::RB)
+                                : make_tile_map(&km, a.k_cache, total, C::TB);
+    if (!kok || !make_tile_map(&vm, a.v_cache, total, C::TB)) return cudaErrorInvalidValue;
+  }
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  auto kern = prefill_ws_kernel<MODE, D, 0, true>;
+  if (!attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const long long grid = (long long)pa.qtiles * pa.splits * a.B * a.Hkv;
+  kern<<<(unsigned)grid, WRoles<D>::THREADS, C::SMEM, st>>>(pa, km, vm);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || pa.splits <= 1) return e;
+  const long long items = (long long)a.B * pa.max_query * a.Hq;
+  cross_merge_kernel<D><<<(unsigned)((items + 7) / 8), 256, 0, st>>>(pa);
+  return cudaGetLastError();
+}
+
+template <int MODE>
+cudaError_t claunch_d(int D, const PrefillArgs& pa, cudaStream_t st) {
+  switch (D) {
+    case 64: return claunch<MODE, 64>(pa, st);
+    case 128: return claunch<MODE, 128>(pa, st);
+    case 256: return claunch<MODE, 256>(pa, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+int cross_query_tile(int D, int G) {
+  return (D == 256 ? WRoles<256>::NQ : WRoles<128>::NQ) * (WROWS / G);
+}
+
+cudaError_t launch_cross(int mode, int D, int G, const DecodeArgs& a, const int* query_start,
+                         int max_query_len, int splits, int split_tiles, cudaStream_t st) {
+  PrefillArgs pa = {};
+  pa.d = a;
+  pa.query_start = query_start;
+  const int tile = cross_query_tile(D, G);
+  pa.qtiles = (max_query_len + tile - 1) / tile;
+  pa.g_shift = __builtin_ctz((unsigned)G);
+  pa.max_query = max_query_len;
+  pa.splits = splits;
+  pa.split_tiles = split_tiles;
+  switch (mode) {
+    case BF16: return claunch_d<BF16>(D, pa, st);
+    case FP8_PER_TENSOR: return claunch_d<FP8_PER_TENSOR>(D, pa, st);
+    case FP8_PER_HEAD: return claunch_d<FP8_PER_HEAD>(D, pa, st);
+    case FP8_PER_TOKEN_HEAD: return claunch_d<FP8_PER_TOKEN_HEAD>(D, pa, st);
+    case INT4_PER_TOKEN_HEAD: return claunch_d<INT4_PER_TOKEN_HEAD>(D, pa, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace kvq

@@ -151,6 +151,16 @@ int decode_warps_per_cta();
 // 128 bytes, box of tile_bytes / 128 rows, 128B swizzle (false on failure).
 bool make_tile_map(CUtensorMap* m, const void* base, long long total_bytes, int tile_bytes);
 
+// A BF16 layer's K buffer as 64-d blocks of 16 cells (false on failure).
+bool make_kblock_map(CUtensorMap* m, const void* base, long long total_bytes, int row_bytes);
+
+// Cross attention of max_query_len queries a sequence at most: DecodeArgs as for
+// the prefill, out_bf16, and for splits > 1 ws_o / ws_ml.
+constexpr int CROSS_KEYS = 64;         // keys per tile; splits are whole tiles
+int cross_query_tile(int D, int G);    // queries of one (sequence, KV head) a CTA takes
+cudaError_t launch_cross(int mode, int D, int G, const DecodeArgs& a, const int* query_start,
+                         int max_query_len, int splits, int split_tiles, cudaStream_t st);
+
 // Device error word of the current device.
 unsigned* error_word();
 

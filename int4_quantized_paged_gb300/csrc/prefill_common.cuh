@@ -13,6 +13,11 @@ struct PrefillArgs {
   DecodeArgs d;                  // caches, scales, block table, context_lens, q, out
   const int* query_start;        // [B + 1]
   int qtiles;                    // query tiles per (sequence, KV head) in the grid
+  // cross attention only
+  int g_shift;                   // log2 of the query heads per KV head
+  int max_query;                 // the caller's bound of a sequence's queries
+  int splits;                    // splits of a sequence's keys, at most
+  int split_tiles;               // key tiles (of 64) per split; the last takes what is left
 };
 
 // 16 raw code bytes -> their f16 (bf16 for BF16) values: 8 (BF16), 16 (FP8)

@@ -85,6 +85,9 @@ _SIGS = {
                                         P, sz, P]),
     "kvq_decode_attention_fixed_scratch": (i32, [P, i32, P, P, P, P, P, P, P, P, i32, P, i32,
                                                  i32, P, i32, P]),
+    "kvq_cross_attention": (i32, [P, i32, P, P, P, P, P, P, P, P, i32, P, P, i32, i32, i32, P, i32,
+                                  P, sz, P]),
+    "kvq_cross_plan": (i32, [P, i32, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(sz)]),
     "kvq_e4m3_encode": (i32, [P, P, i64, P]),
     "kvq_get_device_error": (i32, [P]),
     "kvq_check_bounded_wait": (i32, [i64, P]),
@@ -436,6 +439,34 @@ def kvq_decode_attention_fixed_scratch(ctx: Context, layer: int, q, k_cache, v_c
         ctx, layer, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
         _ptr(k_cache_scale), _ptr(v_cache_scale), _ptr(block_table), mb, _ptr(context_lens), B,
         max_context, _ptr(out), num_workers, _stream(stream)), "kvq_decode_attention_fixed_scratch")
+
+
+def kvq_cross_plan(ctx: Context, layer: int, batch: int, max_query_len: int, max_encoder_len: int,
+                   num_splits: int = 0):
+    """(splits, workspace bytes); max_query_len 0: one query per sequence."""
+    s, w = i32(num_splits), sz()
+    _check(_lib.kvq_cross_plan(ctx, layer, batch, max_query_len, max_encoder_len, ctypes.byref(s),
+                               ctypes.byref(w)), "kvq_cross_plan")
+    return s.value, w.value
+
+
+def kvq_cross_attention(ctx: Context, layer: int, q, k_cache, v_cache, block_table, query_start,
+                        encoder_lens, out, *, max_query_len: int, max_encoder_len: int,
+                        k_scale=None, v_scale=None, k_cache_scale=None, v_cache_scale=None,
+                        num_splits: int = 0, workspace=None, workspace_bytes: Optional[int] = None,
+                        batch: Optional[int] = None, max_blocks_per_seq: Optional[int] = None,
+                        stream=None):
+    """Unmasked attention of each sequence's query rows (query_start None: one row
+    each) to its cached encoder states; bf16 output; see include/kvq.h."""
+    B = encoder_lens.shape[0] if batch is None else batch
+    mb = block_table.shape[1] if max_blocks_per_seq is None else max_blocks_per_seq
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.kvq_cross_attention(
+        ctx, layer, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(k_cache_scale), _ptr(v_cache_scale), _ptr(block_table), mb, _ptr(query_start),
+        _ptr(encoder_lens), B, max_query_len, max_encoder_len, _ptr(out), num_splits,
+        _ptr(workspace), workspace_bytes, _stream(stream)), "kvq_cross_attention")
 
 
 def kvq_e4m3_encode(x, out, n: Optional[int] = None, stream=None):
