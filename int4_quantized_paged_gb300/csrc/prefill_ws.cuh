@@ -161,7 +161,11 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
   volatile int* s_abort = s_have + 4;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_have + 5);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the warp index through a shuffle: the compiler then knows that the role
+  // branches are warp-uniform (descriptors stay in uniform registers, and the
+  // softmax no longer spills)
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   // ---- this CTA's (sequence, KV head, pair of query tiles); latest first.
   // CROSS: the query tiles of one (split, sequence, KV head) are neighbours, so
@@ -350,12 +354,27 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
 
   // ================================================================ roles
   if (warp == RL::PROD) {
-    // ---- producer: key tile t into raw stage (t - t0) % NR; lane s < SUB
-    // copies page tile s.  Page tiles wholly outside [kmin, pmax] are not
-    // fetched.
+    // ---- producer: key tile t into raw stage (t - t0) % NR, page tile by page
+    // tile.  Page tiles wholly outside [kmin, pmax] are not fetched.  The block
+    // ids of 32 page tiles are loaded at once, one per lane and a round ahead, and
+    // every copy is issued by an elected lane from warp-uniform operands (copies
+    // issued by the page tiles' own lanes took a loop over the lanes each).
     int last[NR];                                  // tile index last issued into each stage
 #pragma unroll
     for (int s = 0; s < NR; ++s) last[s] = -1;
+    // block of page tile 32 c + lane (counted from the first key tile): -1 where
+    // nothing is to be fetched
+    auto block_ids = [&](int c) -> int {
+      const int pt = 32 * c + lane;
+      const int pos = t0 * WKT + 16 * pt;
+      if (pt >= SUB * ntl || pos + 16 <= kmin || pos > pmax) return -1;
+      const int blk = __ldg(a.block_table + (long long)b * a.max_blocks + (pos >> a.bs_shift));
+      if (blk >= 0 && blk < a.num_blocks) return blk;
+      atomicOr(a.err, ERR_BAD_INDEX);
+      return -1;
+    };
+    int ids = block_ids(0), ids_next = block_ids(1);
+    unsigned live = __ballot_sync(0xffffffffu, ids >= 0);
     for (int i = 0; i < ntl; ++i) {
       const int st = i % NR;
       if (i >= NR) {
@@ -377,48 +396,46 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
         }
       }
       if (__any_sync(0xffffffffu, *s_abort)) break;
-      const int t = t0 + i;
-      const int pos = t * WKT + 16 * lane;
-      int blk = -1;
-      bool want = false;
-      if (lane < SUB) {
-        want = pos + 16 > kmin && pos <= pmax;
-        if (want) {
-          blk = __ldg(a.block_table + (long long)b * a.max_blocks + (pos >> a.bs_shift));
-          if (blk < 0 || blk >= a.num_blocks) {
-            atomicOr(a.err, ERR_BAD_INDEX);
-            want = false;
-          }
-        }
+      const int at = (SUB * i) & 31;               // the tile's page tiles among the 32
+      if (at == 0 && i > 0) {
+        ids = ids_next;
+        live = __ballot_sync(0xffffffffu, ids >= 0);
+        ids_next = block_ids(SUB * i / 32 + 1);
       }
-      const unsigned fetch = __ballot_sync(0xffffffffu, want);
+      const unsigned fetch = (live >> at) & ((1u << SUB) - 1u);
       uint8_t* base = raw + st * C::RAWS;
       fence_proxy_async();
-      if (lane == 0) {
+      if (elect_one()) {
         s_have[st] = (int)fetch;
         mbar_expect_tx(&raw_full[st], (uint32_t)__popc(fetch) * (2 * C::TB + (C::FETCH ? 128 : 0)));
       }
       __syncwarp();
-      if (want) {
-        const unsigned cell = ((unsigned)blk * (unsigned)a.Hkv + (unsigned)g) * (unsigned)a.bs +
-                              (unsigned)(pos & (a.bs - 1));
-        const int rowc = (int)(((unsigned long long)cell * C::RB) >> 7);
-        if constexpr (C::KDIRECT) {
-          // bf16 K needs no conversion: each 64-d block of the page tile's 16
-          // rows goes to its rows of the K operand (K-major, 128-byte swizzle)
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_tile_3d(k16 + (i % NB) * C::KB + h * (WKT * 128) + lane * (16 * 128), &kmap, 0, h,
-                        (int)cell, &raw_full[st]);
-        } else {
-          tma_tile_2d(base + lane * C::TBP, &kmap, 0, rowc, &raw_full[st]);
+      for (int s = 0; s < SUB; ++s) {
+        const unsigned blk = (unsigned)__shfl_sync(0xffffffffu, ids, at + s);
+        if (((fetch >> s) & 1u) && elect_one()) {
+          const int pos = (t0 + i) * WKT + 16 * s;
+          const unsigned cell = (blk * (unsigned)a.Hkv + (unsigned)g) * (unsigned)a.bs +
+                                (unsigned)(pos & (a.bs - 1));
+          const int rowc = (int)(((unsigned long long)cell * C::RB) >> 7);
+          if constexpr (C::KDIRECT) {
+            // bf16 K needs no conversion: each 64-d block of the page tile's 16
+            // rows goes to its rows of the K operand (K-major, 128-byte swizzle)
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tma_tile_3d(k16 + (i % NB) * C::KB + h * (WKT * 128) + s * (16 * 128), &kmap, 0, h,
+                          (int)cell, &raw_full[st]);
+          } else {
+            tma_tile_2d(base + s * C::TBP, &kmap, 0, rowc, &raw_full[st]);
+          }
+          tma_tile_2d(base + C::VOFF + s * C::TBP, &vmap, 0, rowc, &raw_full[st]);
+          if constexpr (C::FETCH) {
+            float* sc = reinterpret_cast<float*>(base + C::RAW);
+            bulk_copy(sc + 16 * s, a.k_cs + cell, 64, &raw_full[st]);
+            bulk_copy(sc + 16 * (SUB + s), a.v_cs + cell, 64, &raw_full[st]);
+          }
         }
-        tma_tile_2d(base + C::VOFF + lane * C::TBP, &vmap, 0, rowc, &raw_full[st]);
-        if constexpr (C::FETCH) {
-          float* sc = reinterpret_cast<float*>(base + C::RAW);
-          bulk_copy(sc + 16 * lane, a.k_cs + cell, 64, &raw_full[st]);
-          bulk_copy(sc + 16 * (SUB + lane), a.v_cs + cell, 64, &raw_full[st]);
-        }
+        __syncwarp();
       }
       last[st] = i;
     }
