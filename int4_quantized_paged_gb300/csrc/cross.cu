@@ -34,6 +34,8 @@ static_assert(CROSS_KEYS == WKT, "keys per tile");
 // Queries of sequences that one split covers were written by it.
 template <int D>
 __global__ void __launch_bounds__(256) cross_merge_kernel(const PrefillArgs pa) {
+  // launched as a programmatic dependent: the splits' results are visible below
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const DecodeArgs& a = pa.d;
   constexpr int DL = D / 32;                   // elements per lane, as float2 pairs
   const int lane = threadIdx.x & 31;
@@ -78,9 +80,9 @@ __global__ void __launch_bounds__(256) cross_merge_kernel(const PrefillArgs pa) 
   for (int k = 0; k < DL / 2; ++k) out[32 * k] = pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
 }
 
-template <int MODE, int D>
+template <int MODE, int D, bool FEW>
 cudaError_t claunch(const PrefillArgs& pa, cudaStream_t st) {
-  using C = WCfg<MODE, D>;
+  using C = WCfg<MODE, D, FEW>;
   const DecodeArgs& a = pa.d;
   const long long total = a.num_blocks * a.Hkv * a.bs * (long long)C::RB;
   CUtensorMap km = {}, vm = {};
@@ -92,27 +94,40 @@ cudaError_t claunch(const PrefillArgs& pa, cudaStream_t st) {
   static bool attr_set[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto kern = prefill_ws_kernel<MODE, D, 0, true>;
+  auto kern = prefill_ws_kernel<MODE, D, 0, true, FEW>;
   if (!attr_set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const long long grid = (long long)pa.qtiles * pa.splits * a.B * a.Hkv;
-  kern<<<(unsigned)grid, WRoles<D>::THREADS, C::SMEM, st>>>(pa, km, vm);
+  kern<<<(unsigned)grid, WRoles<D, FEW>::THREADS, C::SMEM, st>>>(pa, km, vm);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || pa.splits <= 1) return e;
   const long long items = (long long)a.B * pa.max_query * a.Hq;
-  cross_merge_kernel<D><<<(unsigned)((items + 7) / 8), 256, 0, st>>>(pa);
-  return cudaGetLastError();
+  // its launch overlaps the attention's tail
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((items + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cross_merge_kernel<D>, pa);
 }
 
 template <int MODE>
 cudaError_t claunch_d(int D, const PrefillArgs& pa, cudaStream_t st) {
+  // one query tile's rows at most: the form with two converter groups (at head_dim
+  // 256, which has one query tile anyway, it measured 20 % slower: its operand
+  // buffers leave no room for the second group to work ahead)
+  const bool few = ((long long)pa.max_query << pa.g_shift) <= WROWS;
   switch (D) {
-    case 64: return claunch<MODE, 64>(pa, st);
-    case 128: return claunch<MODE, 128>(pa, st);
-    case 256: return claunch<MODE, 256>(pa, st);
+    case 64: return few ? claunch<MODE, 64, true>(pa, st) : claunch<MODE, 64, false>(pa, st);
+    case 128: return few ? claunch<MODE, 128, true>(pa, st) : claunch<MODE, 128, false>(pa, st);
+    case 256: return claunch<MODE, 256, false>(pa, st);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -120,7 +135,7 @@ cudaError_t claunch_d(int D, const PrefillArgs& pa, cudaStream_t st) {
 }  // namespace
 
 int cross_query_tile(int D, int G) {
-  return (D == 256 ? WRoles<256>::NQ : WRoles<128>::NQ) * (WROWS / G);
+  return (D == 256 ? WRoles<256, false>::NQ : WRoles<128, false>::NQ) * (WROWS / G);
 }
 
 cudaError_t launch_cross(int mode, int D, int G, const DecodeArgs& a, const int* query_start,

@@ -96,7 +96,7 @@ namespace {
 
 template <int MODE, int D, int G>
 cudaError_t wslaunch3(const PrefillArgs& pa0, int max_query_len, cudaStream_t st) {
-  using C = WCfg<MODE, D>;
+  using C = WCfg<MODE, D, false>;
   const DecodeArgs& a = pa0.d;
   const long long total = a.num_blocks * a.Hkv * a.bs * (long long)C::RB;
   CUtensorMap km, vm;
@@ -115,11 +115,11 @@ cudaError_t wslaunch3(const PrefillArgs& pa0, int max_query_len, cudaStream_t st
     attr_set[dev] = true;
   }
   PrefillArgs pa = pa0;
-  const int qp2 = WRoles<D>::NQ * (WROWS / G);      // query positions per CTA
+  const int qp2 = WRoles<D, false>::NQ * (WROWS / G);      // query positions per CTA
   pa.qtiles = (max_query_len + qp2 - 1) / qp2;
   const long long grid = (long long)pa.qtiles * a.B * a.Hkv;
   if (grid <= 0) return cudaSuccess;
-  kern<<<(unsigned)grid, WRoles<D>::THREADS, C::SMEM, st>>>(pa, km, vm);
+  kern<<<(unsigned)grid, WRoles<D, false>::THREADS, C::SMEM, st>>>(pa, km, vm);
   return cudaGetLastError();
 }
 

@@ -8,6 +8,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "async_copy.cuh"
 #include "kvq_internal.h"
 #include "prefill_common.cuh"
@@ -17,7 +19,7 @@
 namespace kvq {
 namespace {
 
-constexpr int WS_CONV = 4;                          // converter warps
+constexpr int WS_CONV = 4;                          // warps of a converter group
 constexpr int WROWS = 128;                          // rows per query tile (the MMA's M)
 
 // A 16-byte shared-memory load that stays after the tensor-memory stores
@@ -33,14 +35,34 @@ __device__ __forceinline__ float4 lds_v4_ordered(const float4* p) {
   return v;
 }
 
+// 32 values of an output row: rounded to bf16, or as they are.
+__device__ __forceinline__ void store_row_bf16(uint16_t* row, const float (&v)[32]) {
+  uint4* dst = reinterpret_cast<uint4*>(row);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                        pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+}
+
+__device__ __forceinline__ void store_row_f32(float* row, const float (&v)[32]) {
+  float4* dst = reinterpret_cast<float4*>(row);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+}
+
 // Warp roles: NQ query tiles per CTA (two at head_dim 64 and 128; one at 256,
 // whose O needs 256 tensor-memory columns), a softmax warpgroup per query
 // tile, then the converters, the producer and the MMA issuer.
-template <int D>
+// FEW (at most 128 rows): one query tile at every head_dim, and two converter
+// groups that take key tiles in turn.  With one query tile a key tile's
+// conversion (1,500 cycles by one group) is a longer step than its MMAs, so the
+// second softmax warpgroup's place goes to a second converter.
+template <int D, bool FEW>
 struct WRoles {
-  static constexpr int NQ = (D == 256) ? 1 : 2;
+  static constexpr int NQ = (D == 256 || FEW) ? 1 : 2;
+  static constexpr int CG = FEW ? 2 : 1;             // converter groups
   static constexpr int SOFT = 4 * NQ;                // softmax warps
-  static constexpr int PROD = SOFT + WS_CONV;        // producer warp
+  static constexpr int PROD = SOFT + CG * WS_CONV;   // producer warp
   static constexpr int MMA = PROD + 1;               // MMA-issuing warp
   static constexpr int THREADS = (MMA + 1) * 32;     // 448 or 320
 };
@@ -48,9 +70,11 @@ constexpr int WKT = 64;                             // keys per tile
 constexpr int WKP = 6;                              // P' = p v_scale 2^(WKP - vexp) < 2^15 (p <= 2^8)
 constexpr float WLAZY = 8.f;                        // the reference max moves when exceeded by this
 // static FP8 scales: P' = p x 2^6 (< 2^14)
-constexpr int CONV_BAR = 1;                         // named barrier of the converter warps
+constexpr int CONV_BAR = 1;                         // named barriers of the converter groups (1, 2)
+constexpr int JOIN_BAR = 3;                         // and of the softmax warps (FEW's epilogue)
+constexpr int Q_BAR = 4;                            // the queries are in place
 
-template <int MODE, int D>
+template <int MODE, int D, bool FEW>
 struct WCfg {
   static constexpr int RB = row_bytes<MODE>(D);
   static constexpr int TB = 16 * RB;                       // one page tile (16 positions)
@@ -76,10 +100,10 @@ struct WCfg {
   static constexpr int VOFF = KDIRECT ? 0 : SUB * TBP;      // V page tiles in a raw stage
   static constexpr int SCB = FETCH ? 2 * SUB * 64 : 0;
   static constexpr int RAWS = (RAW + SCB + 1023) / 1024 * 1024;
-  static constexpr int NQ = WRoles<D>::NQ;
+  static constexpr int NQ = WRoles<D, FEW>::NQ;
   static constexpr int QB = WROWS * D * 2;                  // one query tile: D/64 blocks of 128 x 128 B
-  // queries in shared memory (two query tiles); with one query tile (D 256)
-  // they live in tensor memory instead, the A operand of S
+  // queries in shared memory (two query tiles); with one query tile they live
+  // in tensor memory instead, the A operand of S
   static constexpr int QSM = (NQ == 2) ? 2 * QB : 0;
   static constexpr int KB = WKT * D * 2;                    // one K buffer: D/64 blocks of 64 x 128 B
   static constexpr int VTB = D * WKT * 2;                   // one V^T buffer: D rows of 128 B
@@ -89,11 +113,14 @@ struct WCfg {
   static constexpr int ROWB = 2 * 2 * WROWS * 4;            // row factor and position per row
   static constexpr int BARB = 32 * 8;                       // barriers
   static constexpr int LIMIT = 232448 - 1024;               // per-CTA shared memory, minus slack
-  // operand buffers (K, V^T, scales): three when they fit beside two raw stages
+  // operand buffers (K, V^T, scales): three when they fit beside two raw stages.
+  // FEW: buffers and stages are even in number, so that each converter group
+  // owns every second one and waits for each of their phases.
   static constexpr int fixed_of(int nb) { return QSM + nb * (KB + VTB + SCS) + ROWB + BARB + 64; }
-  static constexpr int NB = (fixed_of(3) + 2 * RAWS <= LIMIT) ? 3 : 2;
+  static constexpr bool fits(int nb, int nr) { return fixed_of(nb) + nr * RAWS <= LIMIT; }
+  static constexpr int NB = FEW ? (fits(4, 2) ? 4 : 2) : (fits(3, 2) ? 3 : 2);
   static constexpr int FIXED = fixed_of(NB);
-  static constexpr int NR = (FIXED + 4 * RAWS <= LIMIT) ? 4 : ((FIXED + 3 * RAWS <= LIMIT) ? 3 : 2);
+  static constexpr int NR = fits(NB, 4) ? 4 : ((!FEW && fits(NB, 3)) ? 3 : 2);
   static constexpr int SMEM = NR * RAWS + FIXED + 1024;
   // Tensor-memory columns.  S/P' buffer b of query tile j: S (fp32, 64
   // columns), then P' (f16 hi in the first 32 columns, lo in the next 32) in
@@ -106,17 +133,18 @@ struct WCfg {
   static constexpr int TCOLS = 512;
   static_assert(NQ == 2 ? 256 + 2 * D <= TCOLS : QCOL + D / 2 <= TCOLS, "tensor memory");
   static_assert(SMEM <= 232448, "shared memory");
+  static_assert(!FEW || WROWS * (D + 1) * 4 <= NR * RAWS + NB * (KB + VTB), "the copies' O");
 };
 
 // CROSS false: causal prefill, G query heads per KV head, fp32 output.
 // CROSS true: attention to all positions of the sequence (no mask), 2^g_shift
-// query heads per KV head, bf16 output, the keys cut into splits.
-template <int MODE, int D, int G, bool CROSS = false>
-__global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
+// query heads per KV head, bf16 output, the keys cut into splits; FEW as above.
+template <int MODE, int D, int G, bool CROSS = false, bool FEW = false>
+__global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
     prefill_ws_kernel(const PrefillArgs pa, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
-  using C = WCfg<MODE, D>;
-  using RL = WRoles<D>;
+  using C = WCfg<MODE, D, FEW>;
+  using RL = WRoles<D, FEW>;
   constexpr int NQ = RL::NQ;
   const DecodeArgs& a = pa.d;
   constexpr int SUB = C::SUB;
@@ -167,6 +195,9 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
+  // the kernel that joins the splits may be launched; it waits for this grid
+  if constexpr (CROSS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   // ---- this CTA's (sequence, KV head, pair of query tiles); latest first.
   // CROSS: the query tiles of one (split, sequence, KV head) are neighbours, so
   // that they read its pages from L2.
@@ -192,6 +223,12 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
   const int qbase = ct * NQ * QP;                           // query index of tile 0, row 0
   const int nq = min(NQ * QP, n_b - qbase);                 // valid query positions here
   const int nqt = (CROSS && nq <= QP) ? 1 : NQ;             // query tiles with rows in use
+  // FEW: 64 rows or fewer stand in the tile two or four times (copy c in the
+  // warps from 4 c / copies on), and the softmax of a copy takes its share of a
+  // key tile's keys, so that every SM sub-partition works on the exponents; the
+  // copies' O are joined in the epilogue like splits.
+  const int copies_shift = !FEW ? 0 : (nq * heads <= 32 ? 2 : (nq * heads <= 64 ? 1 : 0));
+  const int copy_rows = WROWS >> copies_shift;
   int first, pmax, kmin;                                    // first query's position; keys [kmin, pmax]
   bool whole = true;                                        // this CTA sees every key (CROSS)
   if constexpr (CROSS) {
@@ -256,45 +293,69 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
   float ks_static = 1.f;
   if constexpr (MODE == FP8_PER_TENSOR) ks_static = a.k_scale[0];
   if constexpr (MODE == FP8_PER_HEAD) ks_static = a.k_scale[g];
+  // The producer needs none of this and starts its copies at once; converters
+  // take their share of the rows and go on.  Several rows are loaded at a time:
+  // one after the other, their latencies added up to 7 us of a CTA.
   if constexpr (NQ == 2) {
     // into shared memory (K-major, 128-byte swizzle); lane l holds elements
-    // l + 32e of the row
-    for (int R = warp; R < nqt * WROWS; R += RL::THREADS / 32) {
-      const int j = R / WROWS, r = R - j * WROWS;
-      const int h = row_head(r), i = row_query(r);
-      const int qi = j * QP + i;                             // query index within the CTA
-      const bool valid = qi < nq;
-      constexpr int EL = D / 32;
-      float x[EL];
-      float amax = 0.f;
-      if (valid) {
-        const uint16_t* src = a.q + ((long long)(q0 + qbase + qi) * a.Hq + g * heads + h) * D;
+    // l D / 32 ... of a row
+    if (warp != RL::PROD) {
+      constexpr int QW = RL::THREADS / 32 - 1;               // warps that load
+      constexpr int W = D / 64;                              // words (bf16 pairs) per lane
+      constexpr int UR = 8;                                  // rows in flight per warp
+      const int w0 = warp - (warp > RL::PROD ? 1 : 0);
+      for (int Rb = w0; Rb < nqt * WROWS; Rb += UR * QW) {
+        uint32_t x[UR][W];
 #pragma unroll
-        for (int e = 0; e < EL; ++e) {
-          x[e] = __uint_as_float((uint32_t)src[lane + 32 * e] << 16);
-          amax = fmaxf(amax, fabsf(x[e]));
+        for (int u = 0; u < UR; ++u) {
+          const int R = Rb + u * QW;
+          const int j = R / WROWS, r = R - j * WROWS;
+          const int qi = j * QP + row_query(r);              // query index within the CTA
+#pragma unroll
+          for (int e = 0; e < W; ++e) x[u][e] = 0u;
+          if (R < nqt * WROWS && qi < nq) {
+            const uint16_t* src = a.q + ((long long)(q0 + qbase + qi) * a.Hq + g * heads + row_head(r)) * D;
+            if constexpr (W == 2) {
+              const uint2 v = reinterpret_cast<const uint2*>(src)[lane];
+              x[u][0] = v.x;
+              x[u][W - 1] = v.y;
+            } else {
+              x[u][0] = reinterpret_cast<const uint32_t*>(src)[lane];
+            }
+          }
         }
-      } else {
 #pragma unroll
-        for (int e = 0; e < EL; ++e) x[e] = 0.f;
-      }
+        for (int u = 0; u < UR; ++u) {
+          const int R = Rb + u * QW;
+          if (R >= nqt * WROWS) break;
+          const int j = R / WROWS, r = R - j * WROWS;
+          const int qi = j * QP + row_query(r);
+          float amax = 0.f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      int qexp = 0;
-      if (amax > 0.f) qexp = max(((int)(__float_as_uint(amax) >> 23) & 0xFF) - 127, -100);
-      if constexpr (C::BFK) qexp = 14;
-      const float qmul = pow2i(14 - qexp);
-      uint8_t* qt = q16 + j * C::QB;
+          for (int e = 0; e < W; ++e)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[u][e] << 16)),
+                                     fabsf(__uint_as_float(x[u][e] & 0xFFFF0000u))));
 #pragma unroll
-      for (int e = 0; e < EL; ++e) {
-        const int d = lane + 32 * e;
-        const uint16_t h16 = C::BFK ? (uint16_t)(__float_as_uint(x[e]) >> 16)
-                                    : (uint16_t)(pack_f16x2(x[e] * qmul, 0.f) & 0xFFFFu);
-        *reinterpret_cast<uint16_t*>(qt + (d >> 6) * (WROWS * 128) + swc(r, (d & 63) >> 3) + (d & 7) * 2) = h16;
-      }
-      if (lane == 0) {
-        rowf[R] = a.qk_scale * ks_static * pow2i(qexp - 14);
-        rowp[R] = valid ? (CROSS ? first : first + qi) : -1;
+          for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          int qexp = 0;
+          if (amax > 0.f) qexp = max(((int)(__float_as_uint(amax) >> 23) & 0xFF) - 127, -100);
+          if constexpr (C::BFK) qexp = 14;
+          const float qmul = pow2i(14 - qexp);
+          uint32_t y[W];
+#pragma unroll
+          for (int e = 0; e < W; ++e)
+            y[e] = C::BFK ? x[u][e]
+                          : pack_f16x2(__uint_as_float(x[u][e] << 16) * qmul,
+                                       __uint_as_float(x[u][e] & 0xFFFF0000u) * qmul);
+          const int d = lane * (2 * W);
+          uint8_t* dst = q16 + j * C::QB + (d >> 6) * (WROWS * 128) + swc(r, (d & 63) >> 3) + (d & 7) * 2;
+          if constexpr (W == 2) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[W - 1]);
+          else *reinterpret_cast<uint32_t*>(dst) = y[0];
+          if (lane == 0) {
+            rowf[R] = a.qk_scale * ks_static * pow2i(qexp - 14);
+            rowp[R] = qi < nq ? (CROSS ? first : first + qi) : -1;
+          }
+        }
       }
     }
   } else {
@@ -302,16 +363,21 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
     // owns row r (its lane) and stores its D / 2 f16 pairs as columns
     if (warp < RL::SOFT) {
       const int r = warp * 32 + lane;
-      const int h = row_head(r), i = row_query(r);
+      const int rr = FEW ? r & (copy_rows - 1) : r;
+      const int h = row_head(rr), i = row_query(rr);
       const bool valid = i < nq;
       const uint4* src = reinterpret_cast<const uint4*>(
           a.q + ((long long)(q0 + qbase + (valid ? i : 0)) * a.Hq + g * heads + h) * D);
+      constexpr int HELD = D <= 128 ? D / 8 : 16;  // chunks kept in registers between the passes
+      uint4 q8[HELD];
       float amax = 0.f;
-      if (valid) {
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = src[c];
-          const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int cb = 0; cb < D / 8; cb += HELD) {
+#pragma unroll
+        for (int c = 0; c < HELD; ++c) q8[c] = valid ? src[cb + c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < HELD; ++c) {
+          const uint32_t w4[4] = {q8[c].x, q8[c].y, q8[c].z, q8[c].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w4[e] << 16)),
@@ -323,34 +389,43 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
       if constexpr (C::BFK) qexp = 14;
       const float qmul = pow2i(14 - qexp);
       const uint32_t trq = tmem + ((uint32_t)(warp * 32) << 16) + C::QCOL;
-#pragma unroll 1
-      for (int c0 = 0; c0 < D / 2; c0 += 32) {     // 32 columns = 64 elements at a time
-        uint32_t wq[32];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 v = valid ? src[(c0 * 2) / 8 + c] : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+      for (int cb = 0; cb < D / 8; cb += HELD) {
+        if constexpr (HELD < D / 8) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            wq[4 * c + e] = C::BFK ? w4[e]
-                                   : pack_f16x2(__uint_as_float(w4[e] << 16) * qmul,
-                                                __uint_as_float(w4[e] & 0xFFFF0000u) * qmul);
+          for (int c = 0; c < HELD; ++c) q8[c] = valid ? src[cb + c] : make_uint4(0u, 0u, 0u, 0u);
         }
-        uint32_t lo16[16], hi16[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) { lo16[e] = wq[e]; hi16[e] = wq[16 + e]; }
-        tmem_st16_nowait(trq + c0, lo16);
-        tmem_st16_nowait(trq + c0 + 16, hi16);
+        for (int c4 = 0; c4 < HELD; c4 += 4) {     // 16 columns = 32 elements at a time
+          uint32_t wq[16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t w4[4] = {q8[c4 + c].x, q8[c4 + c].y, q8[c4 + c].z, q8[c4 + c].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              wq[4 * c + e] = C::BFK ? w4[e]
+                                     : pack_f16x2(__uint_as_float(w4[e] << 16) * qmul,
+                                                  __uint_as_float(w4[e] & 0xFFFF0000u) * qmul);
+          }
+          tmem_st16_nowait(trq + (cb + c4) * 4, wq);
+        }
       }
       tmem_wait_st();
       rowf[r] = a.qk_scale * ks_static * pow2i(qexp - 14);
       rowp[r] = valid ? (CROSS ? first : first + i) : -1;
     }
   }
-  fence_proxy_async();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  // Q and the rows' factors are in place for the MMA issuer and the softmax
+  constexpr int Q_THREADS = (NQ == 2 ? RL::THREADS - 32 : (RL::SOFT + 1) * 32);
+  if (warp < RL::SOFT || warp == RL::MMA) {
+    fence_proxy_async();
+    tc_fence_before();
+    named_sync(Q_BAR, Q_THREADS);
+    tc_fence_after();
+  } else if (NQ == 2 && warp < RL::PROD) {
+    fence_proxy_async();
+    named_arrive(Q_BAR, Q_THREADS);
+  }
 
   // ================================================================ roles
   if (warp == RL::PROD) {
@@ -445,16 +520,18 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
       for (int s = 0; s < NR; ++s)
         if (last[s] >= 0) (void)mbar_wait(&raw_full[s], (uint32_t)((last[s] / NR) & 1));
   } else if (warp >= RL::SOFT && warp < RL::PROD) {
-    // ---- converters (128 threads)
-    const int ct_ = tid - RL::SOFT * 32;
-    for (int i = 0; i < ntl; ++i) {
+    // ---- converters (groups of 128 threads, taking key tiles in turn)
+    const int cgrp = RL::CG == 1 ? 0 : (warp - RL::SOFT) / WS_CONV;
+    const int ct_ = tid - (RL::SOFT + cgrp * WS_CONV) * 32;
+    const int conv_bar = CONV_BAR + cgrp;
+    for (int i = cgrp; i < ntl; i += RL::CG) {
       const int st = i % NR, buf = i % NB;
       const int t = t0 + i;
       bool ok = mbar_wait(&raw_full[st], (uint32_t)((i / NR) & 1));
       if (i >= NB) ok = mbar_wait(&kv_empty[buf], (uint32_t)((i / NB - 1) & 1)) && ok;
       if (!ok) { *s_abort = 1; atomicOr(a.err, ERR_TIMEOUT); }
       // every converter thread takes the same decision (a barrier reduction)
-      if (named_sync_or(CONV_BAR, WS_CONV * 32, !ok || *s_abort)) break;
+      if (named_sync_or(conv_bar, WS_CONV * 32, !ok || *s_abort)) break;
       const unsigned have = (unsigned)s_have[st];
       const uint8_t* base = raw + st * C::RAWS;
       uint8_t* kb = k16 + buf * C::KB;
@@ -522,7 +599,7 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
           const int e = em ? max((int)em - 127, -100) : 0;
           if (hh == 0) vsm[key] = live ? pow2i(e - 14) : 0.f;
         }
-        named_sync(CONV_BAR, WS_CONV * 32);         // every key's V scale is in place
+        named_sync(conv_bar, WS_CONV * 32);         // every key's V scale is in place
         // V^T: a task is 8 keys x one d pair (one word per key).  Each key's
         // two values are scaled by the inverse of its V scale (a power of two:
         // exact) and packed, keys 2q and 2q + 1 per word, into the rows of
@@ -580,7 +657,7 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
         constexpr int DG = D / 4;                   // d groups of 4
         constexpr int NT = 8 * DG / (WS_CONV * 32); // tasks per thread (4 at D 256, 2 at 128, 1 at 64)
         static_assert(NT * WS_CONV * 32 == 8 * DG, "V^T tasks per converter thread");
-        const int cw = warp - RL::SOFT;              // converter warp 0..3
+        const int cw = (warp - RL::SOFT) & 3;        // converter warp 0..3
 #pragma unroll
         for (int it = 0; it < NT; ++it) {
           int dg, kg;
@@ -630,7 +707,7 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
         // nibbles, read 16x and scaled back exactly).
         constexpr int BG = D / 8;                   // 4-byte groups of a key row
         constexpr int NTI = (8 * BG > WS_CONV * 32) ? 8 * BG / (WS_CONV * 32) : 1;
-        const int cw = warp - RL::SOFT;
+        const int cw = (warp - RL::SOFT) & 3;
 #pragma unroll
         for (int it = 0; it < NTI; ++it) {
         int bg, kg;
@@ -715,7 +792,7 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
         if (ct_ == 0) tinfo[2] = (have == (1u << SUB) - 1u) ? 1 : 0;
       }
       fence_proxy_async();
-      named_sync(CONV_BAR, WS_CONV * 32);
+      named_sync(conv_bar, WS_CONV * 32);
       if (ct_ == 0) {
         mbar_arrive(&raw_empty[st]);                // the raw stage has been read
         mbar_arrive(&kv_full[buf]);
@@ -845,22 +922,19 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
     if constexpr (MODE == FP8_PER_TENSOR) vs_static = a.v_scale[0];
     if constexpr (MODE == FP8_PER_HEAD) vs_static = a.v_scale[g];
     bool ok = true;
-    for (int i = 0; i < ntl; ++i) {
-      const int buf = i % NB, t = t0 + i;
-      // S of this tile in S/P' buffer i & 1 (its P' replaces it there)
-      const int sb = i & 1;
-      const uint32_t tS = trow + C::scol(j, sb), tP = tS;
-      const bool w = __all_sync(0xffffffffu, mbar_wait(&s_full[2 * j + sb], (uint32_t)((i >> 1) & 1)));
-      if (!w && lane == 0) { *s_abort = 1; atomicOr(a.err, ERR_TIMEOUT); }
-      if (!w || __any_sync(0xffffffffu, *s_abort)) { ok = false; break; }
-      if (idle) {
-        mbar_arrive(&p_full[2 * j + sb]);
-        continue;
-      }
+    // Softmax of key tile t (local tile i, operand buffer buf, scores and P' at
+    // tS): NCH chunks of 16 keys from chunk ch0 on.  False when a wait ran out.
+    auto softmax_tile = [&](auto nch, int ch0, int i, int t, int buf, uint32_t tS) -> bool {
+      constexpr int NCH = decltype(nch)::value;
+      const uint32_t tP = tS;                   // P' replaces the scores it came from
       tc_fence_after();
       uint32_t s0[32], s1[32];
-      tmem_ld32_nowait(tS, s0);
-      tmem_ld32_nowait(tS + 32, s1);
+      if constexpr (NCH == 1) {
+        tmem_ld16_nowait(tS + 16 * ch0, s0);
+      } else {
+        tmem_ld32_nowait(tS + 16 * ch0, s0);
+        if constexpr (NCH == 4) tmem_ld32_nowait(tS + 32, s1);
+      }
       tmem_wait_ld();
       const float* ksm = reinterpret_cast<const float*>(scb + buf * C::SCS);
       const float* vsm = ksm + WKT;
@@ -870,12 +944,12 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
       // scores times the K scale (or -inf where masked); four running maxima.
       // The test for a wholly visible tile is taken once, outside the
       // unrolled loops, so neither loop branches per key.
-      const float4* ks4 = reinterpret_cast<const float4*>(ksm);
-      float sv[WKT];
+      const float4* ks4 = reinterpret_cast<const float4*>(ksm) + 4 * ch0;
+      float sv[16 * NCH];
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       if (fast) {
 #pragma unroll
-        for (int k4 = 0; k4 < WKT / 4; ++k4) {
+        for (int k4 = 0; k4 < 4 * NCH; ++k4) {
           const float4 kq = ks4[k4];
           const float ksv[4] = {kq.x, kq.y, kq.z, kq.w};
 #pragma unroll
@@ -889,9 +963,10 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
       } else {
         // keys of this row: [loA, pA] relative to the tile; a key outside the
         // CTA's range or on a page not fetched has scale 0
-        const int klo = loA - t * WKT, khi = pA < 0 ? -1 : pA - t * WKT;
+        const int kt0 = t * WKT + 16 * ch0;
+        const int klo = loA - kt0, khi = pA < 0 ? -1 : pA - kt0;
 #pragma unroll
-        for (int k4 = 0; k4 < WKT / 4; ++k4) {
+        for (int k4 = 0; k4 < 4 * NCH; ++k4) {
           const float4 kq = ks4[k4];
           const float ksv[4] = {kq.x, kq.y, kq.z, kq.w};
 #pragma unroll
@@ -928,7 +1003,7 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
       if (i > 0 && __any_sync(0xffffffffu, al != 1.f)) {
         const bool w2 = __all_sync(0xffffffffu, mbar_wait(&pv_done[j], (uint32_t)((i - 1) & 1)));
         if (!w2 && lane == 0) { *s_abort = 1; atomicOr(a.err, ERR_TIMEOUT); }
-        if (!w2 || __any_sync(0xffffffffu, *s_abort)) { ok = false; break; }
+        if (!w2 || __any_sync(0xffffffffu, *s_abort)) return false;
         tc_fence_after();
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -942,10 +1017,10 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
       // p x 2^k = 2^(score - (mU - k)): the power-of-two range factor k
       // (WKP - vexp, or 6 for static scales) enters the exponent, exactly
       const float mu = ((mU == -INFINITY) ? 0.f : mU) - (C::DYN ? (float)(WKP - vexp) : 6.f);
-      const float4* vs4 = reinterpret_cast<const float4*>(vsm);
+      const float4* vs4 = reinterpret_cast<const float4*>(vsm) + 4 * ch0;
       float lp[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < NCH; ++c) {
         uint32_t hw[8], lw[8];
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
@@ -968,49 +1043,113 @@ __global__ void __launch_bounds__(WRoles<D>::THREADS, 1)
               lw[2 * q4 + h2] = pack_f16x2(x[2 * h2] - f16_lo(h), x[2 * h2 + 1] - f16_hi(h));
           }
         }
-        tmem_st8_nowait(tP + 8 * c, hw);
+        tmem_st8_nowait(tP + 8 * (ch0 + c), hw);
         if constexpr (PTERMS == 2) tmem_st8_nowait(tP + 32 + 8 * c, lw);
       }
+      if constexpr (NCH < 4) {
+        // the other copies' keys have no weight in this one
+        const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int c = NCH; c < 4; ++c) tmem_st8_nowait(tP + 8 * ((ch0 + c) & 3), zero);
+      }
       l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
+      return true;
+    };
+    for (int i = 0; i < ntl; ++i) {
+      const int buf = i % NB, t = t0 + i;
+      // S of this tile in S/P' buffer i & 1
+      const int sb = i & 1;
+      const uint32_t tS = trow + C::scol(j, sb);
+      const bool w = __all_sync(0xffffffffu, mbar_wait(&s_full[2 * j + sb], (uint32_t)((i >> 1) & 1)));
+      if (!w && lane == 0) { *s_abort = 1; atomicOr(a.err, ERR_TIMEOUT); }
+      if (!w || __any_sync(0xffffffffu, *s_abort)) { ok = false; break; }
+      if (idle) {
+        mbar_arrive(&p_full[2 * j + sb]);
+        continue;
+      }
+      if (!FEW || copies_shift == 0)
+        ok = softmax_tile(std::integral_constant<int, 4>{}, 0, i, t, buf, tS);
+      else if constexpr (FEW)
+        ok = copies_shift == 1
+                 ? softmax_tile(std::integral_constant<int, 2>{}, 2 * (warp >> 1), i, t, buf, tS)
+                 : softmax_tile(std::integral_constant<int, 1>{}, warp, i, t, buf, tS);
+      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&p_full[2 * j + sb]);
     }
     // ---- epilogue: out = O x unscale / l (rows without a query store nothing)
     const bool fin = __all_sync(0xffffffffu, mbar_wait(o_fin, 0u));
-    if (ok && fin && !__any_sync(0xffffffffu, *s_abort) && !idle) {
-      tc_fence_after();
-      // O / l: the range factor cancels; static scales multiply by v_scale
-      const float f = l > 0.f ? (C::DYN ? 1.f : vs_static) / l : 0.f;
+    const bool good = ok && fin && !__any_sync(0xffffffffu, *s_abort) && !idle;
+    tc_fence_after();
+    // FEW: copies after the first leave their O / l and the log2 of their weights'
+    // sum (as it was before the range factor) in shared memory, where every copy
+    // and MMA is done
+    float* xo = reinterpret_cast<float*>(smem);                // [D][128]
+    float* xl = xo + D * WROWS;                                // [128]
+    // O / l: the range factor cancels; static scales multiply by v_scale
+    const float f = l > 0.f ? (C::DYN ? 1.f : vs_static) / l : 0.f;
+    float lse = l > 0.f ? mU + log2f(l) + (C::DYN ? (float)(vexp - WKP) : -6.f) : -INFINITY;
+    if constexpr (FEW) {
+      if (copies_shift > 0) {
+        if (good && r >= copy_rows) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float v[32];
+            tmem_ld32(tO + c0, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) xo[(c0 + e) * WROWS + r] = v[e] * f;
+          }
+          xl[r] = lse;
+        }
+        named_sync(JOIN_BAR, RL::SOFT * 32);
+      }
+    }
+    if (good && !(FEW && r >= copy_rows)) {
       const int h = row_head(r), ii = row_query(r);
       if constexpr (CROSS) {
         const int qi = qbase + j * QP + ii;
         const long long orow = (long long)(q0 + qi) * a.Hq + g * heads + h;
-        // a split's result: O / l, and log2 of the sum of the weights as they
-        // were before the range factor
         const long long prow = (((long long)split * a.B + b) * pa.max_query + qi) * a.Hq +
                                g * heads + h;
-        if (!whole && pA >= 0)
-          a.ws_ml[prow] = l > 0.f ? mU + log2f(l) + (C::DYN ? (float)(vexp - WKP) : -6.f) : -INFINITY;
+        // weight of this row's O, and of its copies'
+        float w0 = f, wc[4] = {0.f, 0.f, 0.f, 0.f};
+        const int copies = FEW ? 1 << copies_shift : 1;
+        if (copies > 1) {
+          float top = lse;
+          for (int c = 1; c < copies; ++c) top = fmaxf(top, xl[r + c * copy_rows]);
+          const float ref = top == -INFINITY ? 0.f : top;
+          float sum = ex2(lse - ref);
+          w0 = f * sum;
+#pragma unroll
+          for (int c = 1; c < 4; ++c)
+            if (c < copies) {
+              wc[c] = ex2(xl[r + c * copy_rows] - ref);
+              sum += wc[c];
+            }
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          w0 *= inv;
+#pragma unroll
+          for (int c = 1; c < 4; ++c) wc[c] *= inv;
+          lse = sum > 0.f ? ref + log2f(sum) : -INFINITY;
+        }
+        if (!whole && pA >= 0) a.ws_ml[prow] = lse;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           float v[32];
           tmem_ld32(tO + c0, v);
           if (pA < 0) continue;
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out_bf16 + orow * D + c0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(pack_bf16x2(v[8 * e] * f, v[8 * e + 1] * f),
-                                  pack_bf16x2(v[8 * e + 2] * f, v[8 * e + 3] * f),
-                                  pack_bf16x2(v[8 * e + 4] * f, v[8 * e + 5] * f),
-                                  pack_bf16x2(v[8 * e + 6] * f, v[8 * e + 7] * f));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(a.ws_o + prow * D + c0);
+          for (int e = 0; e < 32; ++e) v[e] *= w0;
+          if constexpr (FEW) {
+            for (int c = 1; c < copies; ++c)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(v[4 * e] * f, v[4 * e + 1] * f, v[4 * e + 2] * f, v[4 * e + 3] * f);
+              for (int e = 0; e < 32; ++e)
+                v[e] = fmaf(c == 1 ? wc[1] : (c == 2 ? wc[2] : wc[3]),
+                            xo[(c0 + e) * WROWS + r + c * copy_rows], v[e]);
           }
+          if (whole) store_row_bf16(a.out_bf16 + orow * D + c0, v);
+          else store_row_f32(a.ws_o + prow * D + c0, v);
         }
       } else {
         float* dst = a.out + ((long long)(q0 + qbase + j * QP + ii) * a.Hq + g * heads + h) * D;
