@@ -30,54 +30,115 @@ namespace {
 
 static_assert(CROSS_KEYS == WKT, "keys per tile");
 
-// Joins the splits of one (query, head) per warp: weights 2^(lse - max).
-// Queries of sequences that one split covers were written by it.
+// Joins the splits of a (query, head) row: weights 2^(lse - max).  WPR warps take
+// a row's splits in turn, so that all of them are in flight at once (19 splits
+// by one warp took 5 us of dependent loads), and meet in shared memory.  Rows of
+// sequences that one split covers were written by it.
+constexpr int MERGE_WARPS = 8;
+
 template <int D>
-__global__ void __launch_bounds__(256) cross_merge_kernel(const PrefillArgs pa) {
+__global__ void __launch_bounds__(MERGE_WARPS * 32) cross_merge_kernel(const PrefillArgs pa, int wpr) {
   // launched as a programmatic dependent: the splits' results are visible below
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const DecodeArgs& a = pa.d;
-  constexpr int DL = D / 32;                   // elements per lane, as float2 pairs
-  const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  constexpr int DL = D / 64;                   // float2 pairs per lane
+  __shared__ float2 s_o[MERGE_WARPS][DL][32];
+  __shared__ float s_ml[MERGE_WARPS][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = warp % wpr;
+  const long long item = (long long)blockIdx.x * (MERGE_WARPS / wpr) + warp / wpr;
   const long long rows = (long long)a.B * pa.max_query;
   const int h = (int)(item % a.Hq);
   const long long r = item / a.Hq;
-  if (r >= rows) return;
-  const int b = (int)(r / pa.max_query), i = (int)(r - (long long)b * pa.max_query);
-  const int q0 = pa.query_start[b], n_b = pa.query_start[b + 1] - q0;
-  const int L = a.context_lens[b];
-  if (i >= n_b || L <= 0 || (long long)L > ((long long)a.max_blocks << a.bs_shift)) return;
-  const int tiles = (L + CROSS_KEYS - 1) / CROSS_KEYS;
-  const int ns = min(pa.splits, (tiles + pa.split_tiles - 1) / pa.split_tiles);
-  if (ns <= 1) return;
-  const long long step = rows * a.Hq;          // partial rows between splits
-  const long long p0 = r * a.Hq + h;
-  float top = -INFINITY;
-  for (int s = lane; s < ns; s += 32) top = fmaxf(top, a.ws_ml[p0 + s * step]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float2 acc[DL / 2];
-#pragma unroll
-  for (int k = 0; k < DL / 2; ++k) acc[k] = make_float2(0.f, 0.f);
-  float sum = 0.f;
-  const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-  for (int s = 0; s < ns; ++s) {
-    const float w = ex2(a.ws_ml[p0 + s * step] - ref);
-    const float2* o = reinterpret_cast<const float2*>(a.ws_o + (p0 + s * step) * D) + lane;
-    sum += w;
-#pragma unroll
-    for (int k = 0; k < DL / 2; ++k) {
-      const float2 v = o[32 * k];
-      acc[k].x = fmaf(w, v.x, acc[k].x);
-      acc[k].y = fmaf(w, v.y, acc[k].y);
+  int ns = 0, q0 = 0, i = 0;
+  if (r < rows) {
+    const int b = (int)(r / pa.max_query);
+    i = (int)(r - (long long)b * pa.max_query);
+    q0 = pa.query_start[b];
+    const int n_b = pa.query_start[b + 1] - q0;
+    const int L = a.context_lens[b];
+    if (i < n_b && L > 0 && (long long)L <= ((long long)a.max_blocks << a.bs_shift)) {
+      const int tiles = (L + CROSS_KEYS - 1) / CROSS_KEYS;
+      ns = min(pa.splits, (tiles + pa.split_tiles - 1) / pa.split_tiles);
     }
   }
+  const bool here = ns > 1;                    // the same for the row's warps
+  const long long step = rows * a.Hq;          // partial rows between splits
+  const long long p0 = r * a.Hq + h;
+  float2 acc[DL];
+#pragma unroll
+  for (int k = 0; k < DL; ++k) acc[k] = make_float2(0.f, 0.f);
+  float top = -INFINITY, sum = 0.f;
+  if (here) {
+    // the running maximum and sum of this warp's splits, eight at a time
+    for (int s0 = part; s0 < ns; s0 += 8 * wpr) {
+      float e[8];
+      float2 v[8][DL];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int s = s0 + u * wpr;
+        e[u] = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < DL; ++k) v[u][k] = make_float2(0.f, 0.f);
+        if (s < ns) {
+          const long long p = p0 + s * step;
+          e[u] = a.ws_ml[p];
+          const float2* o = reinterpret_cast<const float2*>(a.ws_o + p * D) + lane;
+#pragma unroll
+          for (int k = 0; k < DL; ++k) v[u][k] = o[32 * k];
+        }
+      }
+      float m = top;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) m = fmaxf(m, e[u]);
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float old = ex2(top - ref);
+      sum *= old;
+#pragma unroll
+      for (int k = 0; k < DL; ++k) { acc[k].x *= old; acc[k].y *= old; }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float w = ex2(e[u] - ref);
+        sum += w;
+#pragma unroll
+        for (int k = 0; k < DL; ++k) {
+          acc[k].x = fmaf(w, v[u][k].x, acc[k].x);
+          acc[k].y = fmaf(w, v[u][k].y, acc[k].y);
+        }
+      }
+      top = m;
+    }
+  }
+  if (wpr > 1) {
+#pragma unroll
+    for (int k = 0; k < DL; ++k) s_o[warp][k][lane] = acc[k];
+    if (lane == 0) { s_ml[warp][0] = top; s_ml[warp][1] = sum; }
+    __syncthreads();
+    if (part == 0) {
+      float m = top;
+      for (int w = 1; w < wpr; ++w) m = fmaxf(m, s_ml[warp + w][0]);
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float own = ex2(top - ref);
+      sum *= own;
+#pragma unroll
+      for (int k = 0; k < DL; ++k) { acc[k].x *= own; acc[k].y *= own; }
+      for (int w = 1; w < wpr; ++w) {
+        const float f = ex2(s_ml[warp + w][0] - ref);
+        sum = fmaf(f, s_ml[warp + w][1], sum);
+#pragma unroll
+        for (int k = 0; k < DL; ++k) {
+          const float2 v = s_o[warp + w][k][lane];
+          acc[k].x = fmaf(f, v.x, acc[k].x);
+          acc[k].y = fmaf(f, v.y, acc[k].y);
+        }
+      }
+    }
+  }
+  if (!here || part != 0) return;
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   uint32_t* out = reinterpret_cast<uint32_t*>(a.out_bf16 + ((long long)(q0 + i) * a.Hq + h) * D) + lane;
 #pragma unroll
-  for (int k = 0; k < DL / 2; ++k) out[32 * k] = pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
+  for (int k = 0; k < DL; ++k) out[32 * k] = pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
 }
 
 template <int MODE, int D, bool FEW>
@@ -106,16 +167,18 @@ cudaError_t claunch(const PrefillArgs& pa, cudaStream_t st) {
   if (e != cudaSuccess || pa.splits <= 1) return e;
   const long long items = (long long)a.B * pa.max_query * a.Hq;
   // its launch overlaps the attention's tail
+  const int wpr = pa.splits <= 8 ? 1 : (pa.splits <= 16 ? 2 : (pa.splits <= 32 ? 4 : 8));
+  const int per_cta = MERGE_WARPS / wpr;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((items + 7) / 8));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3((unsigned)((items + per_cta - 1) / per_cta));
+  cfg.blockDim = dim3(MERGE_WARPS * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cross_merge_kernel<D>, pa);
+  return cudaLaunchKernelEx(&cfg, cross_merge_kernel<D>, pa, wpr);
 }
 
 template <int MODE>

@@ -174,7 +174,7 @@ __device__ __forceinline__ int upper(const int* incl, int n, int x) {
 }
 
 // ---------------------------------------------------------------- extend
-// Shared memory: five ints for each row of the call.
+// Shared memory: six ints for each row of the call.
 __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(CT)
     extend_kernel(const PageTables t, const ExtendArgs x) {
   cg::cluster_group cl = cg::this_cluster();
@@ -185,6 +185,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(CT)
   int* s_first = s_old + n;                    // first table entry it gets; bit 31: a shared tail's
   int* s_need = s_first + n;                   // inclusive prefix of the blocks needed
   int* s_tok = s_need + n;                     // inclusive prefix of the tokens
+  int* s_seen = s_tok + n;                     // nonzero: the row is named earlier too
   __shared__ int s_warp[CW], s_total, s_most;
   __shared__ long long s_scan[2][CW];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -196,8 +197,24 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(CT)
   const int my_free = count_run<false>(t.ref, run, t.num_blocks, lane);
 
   // ---- the rows, by every CTA alike: thread tid takes rows tid * per ...
-  for (int i = tid; i < n; i += CT) s_row[i] = x.rows[i];
+  for (int i = tid; i < n; i += CT) {
+    s_row[i] = x.rows[i];
+    s_seen[i] = 0;
+  }
   if (tid == 0) s_most = 0;
+  __syncthreads();
+  // rows named twice: each row against the earlier ones, 32 at a time, the pairs
+  // spread over all threads (a loop over them by the row's own thread took 4 us for
+  // 256 rows)
+  for (unsigned w = tid; w < (unsigned)n * ((unsigned)(n + 31) / 32); w += CT) {
+    const int i = (int)(w % (unsigned)n), j0 = (int)(w / (unsigned)n) * 32;
+    if (j0 >= i) continue;
+    const int row = s_row[i];
+    bool hit = false;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) hit |= j0 + j < i && s_row[min(j0 + j, i)] == row;
+    if (hit) s_seen[i] = 1;
+  }
   __syncthreads();
   const int per = (n + CT - 1) / CT;
   long long need_sum = 0, tok_sum = 0;
@@ -208,7 +225,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(CT)
     const int row = s_row[i];
     const int add = x.new_tokens[i];
     bool bad = row < 0 || row >= t.rows || add < 0;
-    for (int j = 0; j < i && !bad; ++j) bad = s_row[j] == row;
+    bad = bad || s_seen[i] != 0;
     const int L = bad ? 0 : t.lens[row];
     bad = bad || !len_ok(t, L) || (long long)L + add > ((long long)t.max_blocks << t.bs_shift);
     int need = 0, first = 0;
@@ -464,10 +481,10 @@ cudaError_t launch_fork(const PageTables& t, const int* parents, const int* chil
 }
 
 cudaError_t launch_extend(const PageTables& t, const ExtendArgs& x, cudaStream_t st) {
-  const int smem = 5 * x.n * (int)sizeof(int);
+  const int smem = 6 * x.n * (int)sizeof(int);
   if (smem > 40 * 1024) {                      // beside about 1 KB of static shared memory
     cudaError_t e = cudaFuncSetAttribute(extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         5 * EXTEND_MAX_ROWS * (int)sizeof(int));
+                                         6 * EXTEND_MAX_ROWS * (int)sizeof(int));
     if (e != cudaSuccess) return e;
   }
   extend_kernel<<<CLUSTER, CT, smem, st>>>(t, x);

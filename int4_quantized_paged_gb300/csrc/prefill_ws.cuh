@@ -258,6 +258,10 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
   const int t0 = kmin / WKT, t1 = pmax / WKT;               // key tiles, inclusive
   const int ntl = t1 - t0 + 1;
 
+  if (warp == RL::PROD && elect_one()) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   if (tid == 0) {
     for (int s = 0; s < NR; ++s) {
       mbar_init(&raw_full[s], 1);

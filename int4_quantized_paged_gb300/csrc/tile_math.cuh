@@ -20,6 +20,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Brings a tensor map that a kernel holds as a parameter on its way early.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 __device__ __forceinline__ void tma_tile_2d(void* dst, const CUtensorMap* map, int x, int y,
                                             uint64_t* bar) {
   asm volatile(
