@@ -539,6 +539,13 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
       const unsigned have = (unsigned)s_have[st];
       const uint8_t* base = raw + st * C::RAWS;
       uint8_t* kb = k16 + buf * C::KB;
+      // The conversions; WHOLE: every key of the tile fetched and in range, without
+      // the test per key that costs the converters a third of their instructions.
+      // Prefill chunks with it: D 256 493 -> 540 TFLOP/s, D 64 390 -> 413, but D 128
+      // 584 -> 567, which keeps the one form; cross attention of few queries 141 ->
+      // 139 us, of prompts the same.
+      auto convert = [&](auto whole_tile) {
+      constexpr bool WHOLE = decltype(whole_tile)::value;
       // K into kb; zeros where nothing was fetched or the position lies
       // outside [kmin, pmax].  Each thread takes NIT chunks; all loads first,
       // then conversions.  (KDIRECT: the producer copied K there; rows of
@@ -554,7 +561,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
           const int key = cc / CPR, ch = cc % CPR;
           const int sub = key >> 4, kr = key & 15;
           const int pos = t * WKT + key;
-          const bool live = ((have >> sub) & 1u) && pos >= kmin && pos <= pmax;
+          const bool live = WHOLE || (((have >> sub) & 1u) && pos >= kmin && pos <= pmax);
           const uint32_t off = swz((uint32_t)(kr * C::RB + ch * 16));
           wk[it] = live ? *reinterpret_cast<const uint4*>(base + sub * C::TBP + off)
                         : make_uint4(0u, 0u, 0u, 0u);
@@ -585,7 +592,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
           const int key = ct_ >> 1, hh = ct_ & 1;
           const int sub = key >> 4, kr = key & 15;
           const int pos = t * WKT + key;
-          const bool live = ((have >> sub) & 1u) && pos >= kmin && pos <= pmax;
+          const bool live = WHOLE || (((have >> sub) & 1u) && pos >= kmin && pos <= pmax);
           uint32_t em = 0;                          // exponent fields (<< 7) of both halves of a word
           if (live) {
 #pragma unroll
@@ -628,7 +635,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
             const int key = 8 * kg + k;
             const int sub = key >> 4, kr = key & 15;
             const int pos = t * WKT + key;
-            const bool live = ((have >> sub) & 1u) && pos >= kmin && pos <= pmax;
+            const bool live = WHOLE || (((have >> sub) & 1u) && pos >= kmin && pos <= pmax);
             x[k] = live ? *reinterpret_cast<const uint32_t*>(base + C::VOFF + sub * C::TBP +
                                                             swz((uint32_t)(kr * C::RB + 4 * dp)))
                         : 0u;
@@ -678,7 +685,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
             const int key = 8 * kg + k;
             const int sub = key >> 4, kr = key & 15;
             const int pos = t * WKT + key;
-            const bool live = ((have >> sub) & 1u) && pos >= kmin && pos <= pmax;
+            const bool live = WHOLE || (((have >> sub) & 1u) && pos >= kmin && pos <= pmax);
             x[k] = live ? *reinterpret_cast<const uint32_t*>(base + (SUB + sub) * C::TBP +
                                                             swz((uint32_t)(kr * C::RB + 4 * dg)))
                         : 0u;
@@ -732,7 +739,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
             const int key = 8 * kg + k;
             const int sub = key >> 4, kr = key & 15;
             const int pos = t * WKT + key;
-            const bool live = ((have >> sub) & 1u) && pos >= kmin && pos <= pmax;
+            const bool live = WHOLE || (((have >> sub) & 1u) && pos >= kmin && pos <= pmax);
             x[k] = live ? *reinterpret_cast<const uint32_t*>(base + (SUB + sub) * C::TBP +
                                                             swz((uint32_t)(kr * C::RB + 4 * bg)))
                         : 0u;
@@ -768,6 +775,12 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
         }
         }
       }
+      };
+      if ((CROSS || D != 128) && have == (1u << SUB) - 1u && t * WKT >= kmin &&
+          t * WKT + WKT - 1 <= pmax)
+        convert(std::true_type{});
+      else
+        convert(std::false_type{});
       {
         // scales: threads 0..63 K, 64..127 V (scale 0: no key)
         float* ksm = reinterpret_cast<float*>(scb + buf * C::SCS);
@@ -949,20 +962,29 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
       // The test for a wholly visible tile is taken once, outside the
       // unrolled loops, so neither loop branches per key.
       const float4* ks4 = reinterpret_cast<const float4*>(ksm) + 4 * ch0;
-      float sv[16 * NCH];
+      uint64_t sv[8 * NCH];                     // pairs of scores
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       if (fast) {
 #pragma unroll
         for (int k4 = 0; k4 < 4 * NCH; ++k4) {
-          const float4 kq = ks4[k4];
-          const float ksv[4] = {kq.x, kq.y, kq.z, kq.w};
+          float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int k = 4 * k4 + e;
-            const float x = __uint_as_float(k < 32 ? s0[k] : s1[k - 32]) * ksv[e];
-            sv[k] = x;
-            m4[e] = fmaxf(m4[e], x);
+            x[e] = __uint_as_float(k < 32 ? s0[k] : s1[k - 32]);
           }
+          uint64_t x01 = pack_f32x2(x[0], x[1]), x23 = pack_f32x2(x[2], x[3]);
+          if constexpr (C::FETCH) {              // else every scale here is 1
+            const float4 kq = lds_v4_ordered(ks4 + k4);
+            x01 = mul_f32x2(x01, pack_f32x2(kq.x, kq.y));
+            x23 = mul_f32x2(x23, pack_f32x2(kq.z, kq.w));
+            unpack_f32x2(x01, x[0], x[1]);
+            unpack_f32x2(x23, x[2], x[3]);
+          }
+          sv[2 * k4] = x01;
+          sv[2 * k4 + 1] = x23;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[e]);
         }
       } else {
         // keys of this row: [loA, pA] relative to the tile; a key outside the
@@ -973,14 +995,16 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
         for (int k4 = 0; k4 < 4 * NCH; ++k4) {
           const float4 kq = ks4[k4];
           const float ksv[4] = {kq.x, kq.y, kq.z, kq.w};
+          float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int k = 4 * k4 + e;
             const bool okk = k >= klo && k <= khi && ksv[e] != 0.f;
-            const float x = okk ? __uint_as_float(k < 32 ? s0[k] : s1[k - 32]) * ksv[e] : -INFINITY;
-            sv[k] = x;
-            m4[e] = fmaxf(m4[e], x);
+            x[e] = okk ? __uint_as_float(k < 32 ? s0[k] : s1[k - 32]) * ksv[e] : -INFINITY;
+            m4[e] = fmaxf(m4[e], x[e]);
           }
+          sv[2 * k4] = pack_f32x2(x[0], x[1]);
+          sv[2 * k4 + 1] = pack_f32x2(x[2], x[3]);
         }
       }
       const float mrow = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * fA;
@@ -1022,7 +1046,8 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
       // (WKP - vexp, or 6 for static scales) enters the exponent, exactly
       const float mu = ((mU == -INFINITY) ? 0.f : mU) - (C::DYN ? (float)(WKP - vexp) : 6.f);
       const float4* vs4 = reinterpret_cast<const float4*>(vsm) + 4 * ch0;
-      float lp[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t fA2 = pack_f32x2(fA, fA), mu2 = pack_f32x2(-mu, -mu);
+      uint64_t lp01 = 0, lp23 = 0;              // four partial sums, as two pairs
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         uint32_t hw[8], lw[8];
@@ -1030,14 +1055,17 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
         for (int q4 = 0; q4 < 4; ++q4) {
           const int k = 16 * c + 4 * q4;
           float x[4];
+          unpack_f32x2(fma_f32x2(sv[k / 2], fA2, mu2), x[0], x[1]);
+          unpack_f32x2(fma_f32x2(sv[k / 2 + 1], fA2, mu2), x[2], x[3]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] = ex2(fmaf(sv[k + e], fA, -mu));
-            lp[e] += x[e];
-          }
+          for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
+          uint64_t x01 = pack_f32x2(x[0], x[1]), x23 = pack_f32x2(x[2], x[3]);
+          lp01 = add_f32x2(lp01, x01);
+          lp23 = add_f32x2(lp23, x23);
           if constexpr (C::DYN) {
             const float4 vq = lds_v4_ordered(vs4 + (k >> 2));
-            x[0] *= vq.x; x[1] *= vq.y; x[2] *= vq.z; x[3] *= vq.w;
+            unpack_f32x2(mul_f32x2(x01, pack_f32x2(vq.x, vq.y)), x[0], x[1]);
+            unpack_f32x2(mul_f32x2(x23, pack_f32x2(vq.z, vq.w)), x[2], x[3]);
           }
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {
@@ -1056,6 +1084,9 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
 #pragma unroll
         for (int c = NCH; c < 4; ++c) tmem_st8_nowait(tP + 8 * ((ch0 + c) & 3), zero);
       }
+      float lp[4];
+      unpack_f32x2(lp01, lp[0], lp[1]);
+      unpack_f32x2(lp23, lp[2], lp[3]);
       l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
       return true;
     };
