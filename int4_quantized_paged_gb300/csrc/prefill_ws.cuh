@@ -106,14 +106,14 @@ struct WCfg {
   // in tensor memory instead, the A operand of S
   static constexpr int QSM = (NQ == 2) ? 2 * QB : 0;
   static constexpr int KB = WKT * D * 2;                    // one K buffer: D/64 blocks of 64 x 128 B
-  static constexpr int VTB = D * WKT * 2;                   // one V^T buffer: D rows of 128 B
+  static constexpr int VTB = WKT * D * 2;                   // one V buffer, as K
   // one scale buffer: K scales, V scales, then ints: V-scale exponent of
   // each 32-key half, whether every page tile was fetched
   static constexpr int SCS = 2 * WKT * 4 + 16;
   static constexpr int ROWB = 2 * 2 * WROWS * 4;            // row factor and position per row
   static constexpr int BARB = 32 * 8;                       // barriers
   static constexpr int LIMIT = 232448 - 1024;               // per-CTA shared memory, minus slack
-  // operand buffers (K, V^T, scales): three when they fit beside two raw stages.
+  // operand buffers (K, V, scales): three when they fit beside two raw stages.
   // FEW: buffers and stages are even in number, so that each converter group
   // owns every second one and waits for each of their phases.
   static constexpr int fixed_of(int nb) { return QSM + nb * (KB + VTB + SCS) + ROWB + BARB + 64; }
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
   uint8_t* raw = smem;                                       // NR stages
   uint8_t* q16 = raw + NR * C::RAWS;                         // 2 query tiles (none for NQ 1)
   uint8_t* k16 = q16 + C::QSM;                               // NB K buffers
-  uint8_t* vt16 = k16 + NB * C::KB;                          // NB V^T buffers
+  uint8_t* vt16 = k16 + NB * C::KB;                          // NB V buffers
   uint8_t* scb = vt16 + NB * C::VTB;                         // NB scale buffers
   float* rowf = reinterpret_cast<float*>(scb + NB * C::SCS); // [2][128] score factor per row
   int* rowp = reinterpret_cast<int*>(rowf + 2 * WROWS);      // [2][128] position (-1: no row)
@@ -539,245 +539,104 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
       const unsigned have = (unsigned)s_have[st];
       const uint8_t* base = raw + st * C::RAWS;
       uint8_t* kb = k16 + buf * C::KB;
-      // The conversions; WHOLE: every key of the tile fetched and in range, without
-      // the test per key that costs the converters a third of their instructions.
-      // Prefill chunks with it: D 256 493 -> 540 TFLOP/s, D 64 390 -> 413, but D 128
-      // 584 -> 567, which keeps the one form; cross attention of few queries 141 ->
-      // 139 us, of prompts the same.
-      auto convert = [&](auto whole_tile) {
-      constexpr bool WHOLE = decltype(whole_tile)::value;
-      // K into kb; zeros where nothing was fetched or the position lies
-      // outside [kmin, pmax].  Each thread takes NIT chunks; all loads first,
-      // then conversions.  (KDIRECT: the producer copied K there; rows of
-      // keys not fetched or outside [kmin, pmax] hold whatever was there, and
-      // the softmax masks their scores by their K scale 0.)
-      constexpr int NIT = WKT * CPR / (WS_CONV * 32);
-      static_assert(NIT * WS_CONV * 32 == WKT * CPR, "chunks per converter thread");
-      if constexpr (!C::KDIRECT) {
-        uint4 wk[NIT];
-#pragma unroll
-        for (int it = 0; it < NIT; ++it) {
-          const int cc = ct_ + it * WS_CONV * 32;
-          const int key = cc / CPR, ch = cc % CPR;
-          const int sub = key >> 4, kr = key & 15;
-          const int pos = t * WKT + key;
-          const bool live = WHOLE || (((have >> sub) & 1u) && pos >= kmin && pos <= pmax);
-          const uint32_t off = swz((uint32_t)(kr * C::RB + ch * 16));
-          wk[it] = live ? *reinterpret_cast<const uint4*>(base + sub * C::TBP + off)
-                        : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int it = 0; it < NIT; ++it) {
-          const int cc = ct_ + it * WS_CONV * 32;
-          const int key = cc / CPR, ch = cc % CPR;
-          const int d0 = ch * EPC;
-          uint4 ok_[4];
-          convert16<MODE>(wk[it], ok_);
-#pragma unroll
-          for (int qq = 0; qq < EPC / 8; ++qq) {
-            const int d = d0 + 8 * qq;
-            *reinterpret_cast<uint4*>(kb + (d >> 6) * (WKT * 128) + swc(key, (d & 63) >> 3)) = ok_[qq];
-          }
-        }
-      }
       uint8_t* vb = vt16 + buf * C::VTB;
-      if constexpr (MODE == BF16) {
-        // V of a BF16 layer.  First the largest exponent e of each key row
-        // (two threads per key, half a row each): the key's V scale is
-        // 2^(e - 14), and the row times 2^(14 - e) has its largest value in
-        // [2^14, 2^15), so every bf16 value down to 2^-28 of it converts to
-        // f16 exactly.
-        float* vsm = reinterpret_cast<float*>(scb + buf * C::SCS) + WKT;
-        {
-          const int key = ct_ >> 1, hh = ct_ & 1;
-          const int sub = key >> 4, kr = key & 15;
+      // The conversions: K and V alike, 64 rows (keys) of D f16 each in 64-d blocks
+      // of 128-byte rows (128-byte swizzle); K is the K-major operand of S, V the
+      // MN-major one of PV, so neither is transposed.  Zeros where nothing was
+      // fetched or the position lies outside [kmin, pmax].  Each thread takes NIT
+      // chunks of each; all loads first, then conversions.  (KDIRECT: the producer
+      // copied K there; rows of keys not fetched or outside the range hold whatever
+      // was there, and the softmax masks their scores by their K scale 0.)
+      // WHOLE: every key of the tile fetched and in range, without the test per key.
+      auto convert = [&](auto whole_tile) {
+        constexpr bool WHOLE = decltype(whole_tile)::value;
+        constexpr int NIT = WKT * CPR / (WS_CONV * 32);
+        static_assert(NIT * WS_CONV * 32 == WKT * CPR, "chunks per converter thread");
+        // chunk it of this thread: neighbouring eight lanes take the low chunks of
+        // one key and the high ones of the next, whose rows are swizzled apart, so
+        // that the stores of both 64-d blocks meet each bank once
+        auto key_of = [&](int it, int& ch) -> int {
+          const int cc = ct_ + it * WS_CONV * 32;
+          const int row = cc / CPR;
+          ch = cc % CPR;
+          return (CPR >= 8 && EPC == 16) ? (row & ~1) | ((row ^ (ch >> 2)) & 1) : row;
+        };
+        auto is_live = [&](int key) -> bool {
           const int pos = t * WKT + key;
-          const bool live = WHOLE || (((have >> sub) & 1u) && pos >= kmin && pos <= pmax);
-          uint32_t em = 0;                          // exponent fields (<< 7) of both halves of a word
-          if (live) {
+          return WHOLE || (((have >> (key >> 4)) & 1u) && pos >= kmin && pos <= pmax);
+        };
+        auto load = [&](int off, int key, int ch) -> uint4 {
+          return is_live(key) ? *reinterpret_cast<const uint4*>(
+                                    base + off + (key >> 4) * C::TBP +
+                                    swz((uint32_t)((key & 15) * C::RB + ch * 16)))
+                              : make_uint4(0u, 0u, 0u, 0u);
+        };
+        auto store = [&](uint8_t* dst, int key, int d, uint4 v) {
+          *reinterpret_cast<uint4*>(dst + (d >> 6) * (WKT * 128) + swc(key, (d & 63) >> 3)) = v;
+        };
+        if constexpr (MODE == BF16) {
+          // V of a BF16 layer.  First the largest exponent e of each key row (two
+          // threads per key, half a row each): the key's V scale is 2^(e - 14), and
+          // the row times 2^(14 - e) has its largest value in [2^14, 2^15), so every
+          // bf16 value down to 2^-28 of it converts to f16 exactly.
+          float* vsm = reinterpret_cast<float*>(scb + buf * C::SCS) + WKT;
+          {
+            const int key = ct_ >> 1, hh = ct_ & 1;
+            uint32_t em = 0;                          // exponent fields (<< 7) of both halves of a word
 #pragma unroll
             for (int c = 0; c < CPR / 2; ++c) {
-              const uint4 w = *reinterpret_cast<const uint4*>(
-                  base + C::VOFF + sub * C::TBP + swz((uint32_t)(kr * C::RB + (hh * (CPR / 2) + c) * 16)));
+              const uint4 w = load(C::VOFF, key, hh * (CPR / 2) + c);
               em = __vmaxu2(em, w.x & 0x7F807F80u);
               em = __vmaxu2(em, w.y & 0x7F807F80u);
               em = __vmaxu2(em, w.z & 0x7F807F80u);
               em = __vmaxu2(em, w.w & 0x7F807F80u);
             }
+            em = max(em & 0xFFFFu, em >> 16) >> 7;    // biased exponent, 0 for zeros
+            em = max(em, __shfl_xor_sync(0xffffffffu, em, 1));
+            const int e = em ? max((int)em - 127, -100) : 0;
+            if (hh == 0) vsm[key] = is_live(key) ? pow2i(e - 14) : 0.f;
           }
-          em = max(em & 0xFFFFu, em >> 16) >> 7;    // biased exponent, 0 for zeros
-          em = max(em, __shfl_xor_sync(0xffffffffu, em, 1));
-          const int e = em ? max((int)em - 127, -100) : 0;
-          if (hh == 0) vsm[key] = live ? pow2i(e - 14) : 0.f;
-        }
-        named_sync(conv_bar, WS_CONV * 32);         // every key's V scale is in place
-        // V^T: a task is 8 keys x one d pair (one word per key).  Each key's
-        // two values are scaled by the inverse of its V scale (a power of two:
-        // exact) and packed, keys 2q and 2q + 1 per word, into the rows of
-        // d = 2 dp (low halves) and 2 dp + 1 (high halves).  Consecutive
-        // lanes take consecutive d pairs of the same keys (one 128-byte row
-        // per load), and lanes with bit 2 set store their odd row first, so
-        // that each 8-lane phase of a store meets every bank once.
-        constexpr int DP = D / 2;
-        constexpr int NTB = 8 * DP / (WS_CONV * 32);
-        static_assert(NTB * WS_CONV * 32 == 8 * DP, "V^T tasks per converter thread");
+          named_sync(conv_bar, WS_CONV * 32);         // every key's V scale is in place
 #pragma unroll
-        for (int it = 0; it < NTB; ++it) {
-          const int task = ct_ + it * WS_CONV * 32;
-          const int dp = task % DP, kg = task / DP;
-          const float4 s0 = *reinterpret_cast<const float4*>(vsm + 8 * kg);
-          const float4 s1 = *reinterpret_cast<const float4*>(vsm + 8 * kg + 4);
-          const float sk[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-          uint32_t x[8];
-          float inv[8];
+          for (int it = 0; it < NIT; ++it) {
+            int ch;
+            const int key = key_of(it, ch);
+            if constexpr (!C::KDIRECT) store(kb, key, 8 * ch, load(0, key, ch));
+            // 2^(14 - e) from 2^(e - 14): exact; 2^127 for a key with no data (its values are 0)
+            const float inv = __uint_as_float((254u - (__float_as_uint(vsm[key]) >> 23)) << 23);
+            const uint4 w = load(C::VOFF, key, ch);
+            const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+            uint32_t y[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int key = 8 * kg + k;
-            const int sub = key >> 4, kr = key & 15;
-            const int pos = t * WKT + key;
-            const bool live = WHOLE || (((have >> sub) & 1u) && pos >= kmin && pos <= pmax);
-            x[k] = live ? *reinterpret_cast<const uint32_t*>(base + C::VOFF + sub * C::TBP +
-                                                            swz((uint32_t)(kr * C::RB + 4 * dp)))
-                        : 0u;
-            // 2^(14 - e) from 2^(e - 14); 2^127 for a key with no data (its values are 0)
-            inv[k] = __uint_as_float((254u - (__float_as_uint(sk[k]) >> 23)) << 23);
+            for (int e = 0; e < 4; ++e)
+              y[e] = pack_f16x2(__uint_as_float(w4[e] << 16) * inv,
+                                __uint_as_float(w4[e] & 0xFFFF0000u) * inv);
+            store(vb, key, 8 * ch, make_uint4(y[0], y[1], y[2], y[3]));
           }
-          uint32_t ev[4], od[4];
+        } else {
+          uint4 wk[NIT], wv[NIT];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            ev[q] = pack_f16x2(__uint_as_float(x[2 * q] << 16) * inv[2 * q],
-                               __uint_as_float(x[2 * q + 1] << 16) * inv[2 * q + 1]);
-            od[q] = pack_f16x2(__uint_as_float(x[2 * q] & 0xFFFF0000u) * inv[2 * q],
-                               __uint_as_float(x[2 * q + 1] & 0xFFFF0000u) * inv[2 * q + 1]);
-          }
-          const uint4 E = make_uint4(ev[0], ev[1], ev[2], ev[3]);
-          const uint4 O = make_uint4(od[0], od[1], od[2], od[3]);
-          const bool swp = (lane >> 2) & 1;
-          *reinterpret_cast<uint4*>(vb + swc(2 * dp + (swp ? 1 : 0), kg)) = swp ? O : E;
-          *reinterpret_cast<uint4*>(vb + swc(2 * dp + (swp ? 0 : 1), kg)) = swp ? E : O;
-        }
-      }
-      if constexpr (MODE != INT4_PER_TOKEN_HEAD && MODE != BF16) {
-        // V^T straight from the raw FP8 codes: a task is 8 keys x 4 d.  Its
-        // 8 words (one per key: codes of d..d+3) are transposed in registers
-        // into 4 rows of 8 codes each, converted, and stored as one 16-byte
-        // chunk per d row.  Lane-to-task map: consecutive lanes take
-        // consecutive d groups, and the key group turns with the lane pair and
-        // the warp, so the 4-byte loads and the 16-byte stores of a warp meet
-        // no bank twice.
-        constexpr int DG = D / 4;                   // d groups of 4
-        constexpr int NT = 8 * DG / (WS_CONV * 32); // tasks per thread (4 at D 256, 2 at 128, 1 at 64)
-        static_assert(NT * WS_CONV * 32 == 8 * DG, "V^T tasks per converter thread");
-        const int cw = (warp - RL::SOFT) & 3;        // converter warp 0..3
-#pragma unroll
-        for (int it = 0; it < NT; ++it) {
-          int dg, kg;
-          if constexpr (DG > 32) {                  // D 256: two sweeps of 32 d groups
-            dg = lane + 32 * (it & 1);
-            kg = (((lane >> 1) + cw) & 3) + 4 * (it >> 1);
-          } else {
-            dg = lane % DG;
-            kg = (((dg >> 1) + cw) & 3) + 4 * (it + lane / DG);
-          }
-          uint32_t x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int key = 8 * kg + k;
-            const int sub = key >> 4, kr = key & 15;
-            const int pos = t * WKT + key;
-            const bool live = WHOLE || (((have >> sub) & 1u) && pos >= kmin && pos <= pmax);
-            x[k] = live ? *reinterpret_cast<const uint32_t*>(base + (SUB + sub) * C::TBP +
-                                                            swz((uint32_t)(kr * C::RB + 4 * dg)))
-                        : 0u;
-          }
-          uint32_t lo[4], hi[4];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t* y = x + 4 * half;
-            const uint32_t t0 = __byte_perm(y[0], y[1], 0x5140), t1 = __byte_perm(y[0], y[1], 0x7362);
-            const uint32_t t2 = __byte_perm(y[2], y[3], 0x5140), t3 = __byte_perm(y[2], y[3], 0x7362);
-            uint32_t* o = half ? hi : lo;
-            o[0] = __byte_perm(t0, t2, 0x5410);     // byte dd of keys 0..3 (or 4..7)
-            o[1] = __byte_perm(t0, t2, 0x7632);
-            o[2] = __byte_perm(t1, t3, 0x5410);
-            o[3] = __byte_perm(t1, t3, 0x7632);
+          for (int it = 0; it < NIT; ++it) {
+            int ch;
+            const int key = key_of(it, ch);
+            wk[it] = load(0, key, ch);
+            wv[it] = load(C::VOFF, key, ch);
           }
 #pragma unroll
-          for (int dd = 0; dd < 4; ++dd) {
-            uint4 v;
-            e4m3x4_f16(lo[dd], v.x, v.y);
-            e4m3x4_f16(hi[dd], v.z, v.w);
-            *reinterpret_cast<uint4*>(vb + swc(4 * dg + dd, kg)) = v;
+          for (int it = 0; it < NIT; ++it) {
+            int ch;
+            const int key = key_of(it, ch);
+            uint4 o[4];
+            convert16<MODE>(wk[it], o);
+#pragma unroll
+            for (int q = 0; q < EPC / 8; ++q) store(kb, key, ch * EPC + 8 * q, o[q]);
+            convert16<MODE>(wv[it], o);
+#pragma unroll
+            for (int q = 0; q < EPC / 8; ++q) store(vb, key, ch * EPC + 8 * q, o[q]);
           }
         }
-      }
-      if constexpr (MODE == INT4_PER_TOKEN_HEAD) {
-        // V^T straight from the raw INT4 codes: a task is 8 keys x 4 bytes
-        // (8 d).  The 8 words are transposed as for FP8; byte bb of 4 keys
-        // then gives the f16 values of d = 2bb (low nibbles) and 2bb + 1 (high
-        // nibbles, read 16x and scaled back exactly).
-        constexpr int BG = D / 8;                   // 4-byte groups of a key row
-        constexpr int NTI = (8 * BG > WS_CONV * 32) ? 8 * BG / (WS_CONV * 32) : 1;
-        const int cw = (warp - RL::SOFT) & 3;
-#pragma unroll
-        for (int it = 0; it < NTI; ++it) {
-        int bg, kg;
-        if constexpr (BG >= 32) {                   // D 256: 256 tasks, two per thread
-          bg = lane;
-          kg = (((lane >> 1) + cw) & 3) + 4 * it;
-        } else if constexpr (BG >= 16) {            // 128 tasks, one per thread
-          bg = lane % BG;
-          kg = (((bg >> 1) + cw) & 3) + 4 * (lane / BG);
-        } else {                                    // 64 tasks: the first 64 threads
-          bg = ct_ % BG;
-          kg = ct_ / BG;
-        }
-        if (kg < 8) {
-          uint32_t x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int key = 8 * kg + k;
-            const int sub = key >> 4, kr = key & 15;
-            const int pos = t * WKT + key;
-            const bool live = WHOLE || (((have >> sub) & 1u) && pos >= kmin && pos <= pmax);
-            x[k] = live ? *reinterpret_cast<const uint32_t*>(base + (SUB + sub) * C::TBP +
-                                                            swz((uint32_t)(kr * C::RB + 4 * bg)))
-                        : 0u;
-          }
-          uint32_t lo[4], hi[4];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t* y = x + 4 * half;
-            const uint32_t t0 = __byte_perm(y[0], y[1], 0x5140), t1 = __byte_perm(y[0], y[1], 0x7362);
-            const uint32_t t2 = __byte_perm(y[2], y[3], 0x5140), t3 = __byte_perm(y[2], y[3], 0x7362);
-            uint32_t* o = half ? hi : lo;
-            o[0] = __byte_perm(t0, t2, 0x5410);
-            o[1] = __byte_perm(t0, t2, 0x7632);
-            o[2] = __byte_perm(t1, t3, 0x5410);
-            o[3] = __byte_perm(t1, t3, 0x7632);
-          }
-#pragma unroll
-          for (int bb = 0; bb < 4; ++bb) {
-            uint32_t ev[4], od[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              // keys 2q, 2q + 1: bytes (q & 1) * 2 and +1 of lo or hi
-              const uint32_t wq = (q < 2) ? lo[bb] : hi[bb];
-              const uint32_t pr = __byte_perm(wq, 0u, (q & 1) ? 0x7372 : 0x7170);
-              ev[q] = nib2_f16x2<0>(pr);
-              const uint32_t h16 = nib2_f16x2<1>(pr);
-              asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(od[q]) : "r"(h16), "r"(0x2C002C00u));   // x 1/16
-            }
-            const int d = 8 * bg + 2 * bb;
-            *reinterpret_cast<uint4*>(vb + swc(d, kg)) = make_uint4(ev[0], ev[1], ev[2], ev[3]);
-            *reinterpret_cast<uint4*>(vb + swc(d + 1, kg)) = make_uint4(od[0], od[1], od[2], od[3]);
-          }
-        }
-        }
-      }
       };
-      if ((CROSS || D != 128) && have == (1u << SUB) - 1u && t * WKT >= kmin &&
-          t * WKT + WKT - 1 <= pmax)
+      if (have == (1u << SUB) - 1u && t * WKT >= kmin && t * WKT + WKT - 1 <= pmax)
         convert(std::true_type{});
       else
         convert(std::false_type{});
@@ -819,7 +678,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
     // ---- MMA issuer: one elected lane issues and commits (elect.sync picks
     // the same lane each time: the warp is converged); the warp waits together
     constexpr uint32_t IDS = mma_idesc<C::BFK>(WROWS, WKT);   // bf16 Q and K for BF16 layers
-    constexpr uint32_t IDO = mma_idesc<false>(WROWS, D);
+    constexpr uint32_t IDO = mma_idesc<false>(WROWS, D) | MMA_B_MN_MAJOR;
     auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
       const bool w = __all_sync(0xffffffffu, mbar_wait(bar, par));
       if (!w && lane == 0) { *s_abort = 1; atomicOr(a.err, ERR_TIMEOUT); }
@@ -828,7 +687,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
     // Descriptors of the operand buffers' starts; an operand at byte offset
     // o is the start's descriptor plus o / 16 (the 14-bit address field
     // cannot carry: shared memory ends below 2^18 bytes)
-    const uint64_t dq = sw128_desc(q16), dk = sw128_desc(k16), dv = sw128_desc(vt16);
+    const uint64_t dq = sw128_desc(q16), dk = sw128_desc(k16), dv = sw128_mn_desc(vt16, WKT * 128);
     // S_j = Q_j K^T from K buffer kbuf into S buffer sb of query tile j (Q
     // from shared memory with two query tiles, from tensor memory with one)
     auto issue_s = [&](int j, int kbuf, int sb) {
@@ -850,8 +709,8 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
       }
       __syncwarp();
     };
-    // O_j += P'_j V, both terms of the split, P' from S/P' buffer sb, V^T
-    // from buffer vbuf
+    // O_j += P'_j V, every term of the split, P' from S/P' buffer sb, V from
+    // buffer vbuf
     auto issue_pv = [&](int j, int vbuf, int sb, bool acc) {
       const uint64_t vb = dv + (uint64_t)(vbuf * (C::VTB >> 4));
       const uint32_t td = tmem + C::ocol(j);
@@ -862,7 +721,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
         for (int h = 0; h < PTERMS; ++h)
 #pragma unroll
           for (int kk = 0; kk < WKT / 16; ++kk)
-            umma_tmem_a(td, ta + 32 * h + 8 * kk, vb + (uint64_t)(kk * 2), IDO, acc || h > 0 || kk > 0);
+            umma_tmem_a(td, ta + 32 * h + 8 * kk, vb + (uint64_t)(kk * (16 * 128 >> 4)), IDO, acc || h > 0 || kk > 0);
       }
       __syncwarp();
     };

@@ -24,6 +24,22 @@ __device__ __forceinline__ uint64_t sw128_desc(const void* p) {
   return d;
 }
 
+// As sw128_desc for an MN-major operand: rows of 128 bytes hold 64 f16 of M or
+// N, one row per K; 8-row groups (8 of K) 1024 bytes apart, the next 64 of M or N
+// `block` bytes on.  The start address may be advanced by whole row groups along K.
+__device__ __forceinline__ uint64_t sw128_mn_desc(const void* p, uint32_t block) {
+  const uint32_t a = smem_u32(p);
+  uint64_t d = (uint64_t)((a >> 4) & 0x3FFFu);      // start address / 16
+  d |= (uint64_t)(block >> 4) << 16;                 // stride between 64-element blocks
+  d |= (uint64_t)(1024 >> 4) << 32;                  // stride between 8-row groups
+  d |= (uint64_t)1 << 46;                            // descriptor version
+  d |= (uint64_t)2 << 61;                            // 128-byte swizzle
+  return d;
+}
+
+// Bit of an instruction descriptor: the B operand is MN-major.
+constexpr uint32_t MMA_B_MN_MAJOR = 1u << 16;
+
 // Instruction descriptor: f32 accumulator, f16 (BF false) or bf16 operands,
 // both K-major, M x N.
 template <bool BF>
