@@ -52,7 +52,8 @@ __device__ __forceinline__ void store_row_f32(float* row, const float (&v)[32]) 
 
 // Warp roles: NQ query tiles per CTA (two at head_dim 64 and 128; one at 256,
 // whose O needs 256 tensor-memory columns), a softmax warpgroup per query
-// tile, then the converters, the producer and the MMA issuer.
+// tile, then the converters, the producer and two MMA issuers, of S and of PV
+// (FEW: one of both).
 // FEW (at most 128 rows): one query tile at every head_dim, and two converter
 // groups that take key tiles in turn.  With one query tile a key tile's
 // conversion (1,500 cycles by one group) is a longer step than its MMAs, so the
@@ -63,8 +64,9 @@ struct WRoles {
   static constexpr int CG = FEW ? 2 : 1;             // converter groups
   static constexpr int SOFT = 4 * NQ;                // softmax warps
   static constexpr int PROD = SOFT + CG * WS_CONV;   // producer warp
-  static constexpr int MMA = PROD + 1;               // MMA-issuing warp
-  static constexpr int THREADS = (MMA + 1) * 32;     // 448 or 320
+  static constexpr int MMA_S = PROD + 1;             // warp that issues S
+  static constexpr int MMA_PV = FEW ? MMA_S : PROD + 2;   // and the one that issues PV
+  static constexpr int THREADS = (MMA_PV + 1) * 32;  // 480, 448 or 352
 };
 constexpr int WKT = 64;                             // keys per tile
 constexpr int WKP = 6;                              // P' = p v_scale 2^(WKP - vexp) < 2^15 (p <= 2^8)
@@ -183,8 +185,11 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
   // the MMA issuer waits for its tile t, and a barrier per query tile would
   // then complete two phases ahead of its waiter.
   uint64_t* p_full = s_full + 4;
-  uint64_t* pv_done = p_full + 4;                            // [2] MMA (commit) -> softmax j
-  uint64_t* o_fin = pv_done + 2;                             // MMA (commit) -> softmax, at the end
+  // PV (commit) -> S issuer and softmax j, per S/P' buffer for the same reason
+  uint64_t* pv_done = p_full + 4;
+  uint64_t* o_fin = pv_done + 4;                             // PV (commit) -> softmax, at the end
+  uint64_t* s_fin = o_fin + 1;                               // the S issuer's own end
+  static_assert(2 * NR + 2 * NB + 3 * 4 + 2 <= 32, "barriers");
   int* s_have = reinterpret_cast<int*>(bars + 32);           // [NR] fetched page tiles per stage
   volatile int* s_abort = s_have + 4;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_have + 5);
@@ -275,8 +280,9 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 4 * 32);
     }
-    for (int s = 0; s < 2; ++s) mbar_init(&pv_done[s], 1);
+    for (int s = 0; s < 4; ++s) mbar_init(&pv_done[s], 1);
     mbar_init(o_fin, 1);
+    mbar_init(s_fin, 1);
     mbar_init_fence();
     *s_abort = 0;
   }
@@ -419,14 +425,14 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
       rowp[r] = valid ? (CROSS ? first : first + i) : -1;
     }
   }
-  // Q and the rows' factors are in place for the MMA issuer and the softmax
+  // Q and the rows' factors are in place for the S issuer and the softmax
   constexpr int Q_THREADS = (NQ == 2 ? RL::THREADS - 32 : (RL::SOFT + 1) * 32);
-  if (warp < RL::SOFT || warp == RL::MMA) {
+  if (warp < RL::SOFT || warp == RL::MMA_S) {
     fence_proxy_async();
     tc_fence_before();
     named_sync(Q_BAR, Q_THREADS);
     tc_fence_after();
-  } else if (NQ == 2 && warp < RL::PROD) {
+  } else if (NQ == 2 && warp != RL::PROD) {
     fence_proxy_async();
     named_arrive(Q_BAR, Q_THREADS);
   }
@@ -674,9 +680,13 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
         mbar_arrive(&kv_full[buf]);
       }
     }
-  } else if (warp == RL::MMA) {
-    // ---- MMA issuer: one elected lane issues and commits (elect.sync picks
-    // the same lane each time: the warp is converged); the warp waits together
+  } else if (warp == RL::MMA_S || warp == RL::MMA_PV) {
+    // ---- MMA issuers: one elected lane issues and commits (elect.sync picks the
+    // same lane each time: the warp is converged); the warp waits together.  S and
+    // PV have a warp each: one warp for both that waited for the P' of a query
+    // tile held up the other tile's next scores, and its waits and issues alone
+    // took 1,900 cycles of a key tile's 2,700.  With one query tile (FEW) there is
+    // nothing to hold up, and a second polling warp costs more (134 -> 143 us).
     constexpr uint32_t IDS = mma_idesc<C::BFK>(WROWS, WKT);   // bf16 Q and K for BF16 layers
     constexpr uint32_t IDO = mma_idesc<false>(WROWS, D) | MMA_B_MN_MAJOR;
     auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
@@ -721,57 +731,54 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
         for (int h = 0; h < PTERMS; ++h)
 #pragma unroll
           for (int kk = 0; kk < WKT / 16; ++kk)
-            umma_tmem_a(td, ta + 32 * h + 8 * kk, vb + (uint64_t)(kk * (16 * 128 >> 4)), IDO, acc || h > 0 || kk > 0);
+            umma_tmem_a(td, ta + 32 * h + 8 * kk, vb + (uint64_t)(kk * (16 * 128 >> 4)), IDO,
+                        acc || h > 0 || kk > 0);
+        umma_commit(&pv_done[2 * j + sb]);
       }
       __syncwarp();
     };
-    // S of key tile t goes into S/P' buffer t & 1 of each query tile, two
-    // tiles ahead of the softmax that reads it: S_j(t+2) is issued once
-    // PV_j(t), the last reader of that buffer's P', has completed, so the
-    // softmax of a query tile finds its next scores ready when it finishes
-    if (wait(&kv_full[0], 0u)) {
+    // S of key tile i goes into S/P' buffer i & 1 of each query tile, two tiles
+    // ahead of the softmax that reads it: S_j(i) is issued once PV_j(i-2), the
+    // last reader of that buffer's P', has completed, so the softmax of a query
+    // tile finds its next scores ready when it finishes
+    auto scores = [&](int i) -> bool {
+      bool go = wait(&kv_full[i % NB], (uint32_t)((i / NB) & 1));
 #pragma unroll
-      for (int j = 0; j < NQ; ++j)
-        if (j < nqt) issue_s(j, 0, 0);
+      for (int j = 0; j < NQ; ++j) {
+        if (!go || j >= nqt) break;
+        if (i >= 2) go = wait(&pv_done[2 * j + (i & 1)], (uint32_t)(((i >> 1) - 1) & 1));
+        if (go) issue_s(j, i % NB, i & 1);
+      }
+      return go;
+    };
+    auto values = [&](int i) -> bool {
       bool go = true;
-      if (ntl > 1) {
-        go = wait(&kv_full[1 % NB], (uint32_t)((1 / NB) & 1));
-        if (go)
 #pragma unroll
-          for (int j = 0; j < NQ; ++j)
-            if (j < nqt) issue_s(j, 1 % NB, 1);
+      for (int j = 0; j < NQ; ++j) {
+        if (!go || j >= nqt) break;
+        go = wait(&p_full[2 * j + (i & 1)], (uint32_t)((i >> 1) & 1));
+        if (go) issue_pv(j, i % NB, i & 1, i > 0);
       }
-      for (int i = 0; go && i < ntl; ++i) {
-        const int buf = i % NB, sb = i & 1;
-#pragma unroll
-        for (int j = 0; j < NQ; ++j) {
-          if (j >= nqt) break;
-          if (!wait(&p_full[2 * j + sb], (uint32_t)((i >> 1) & 1))) { go = false; break; }
-          issue_pv(j, buf, sb, i > 0);
-          if (elect_one()) umma_commit(&pv_done[j]);
-          __syncwarp();
-        }
-        if (!go) break;
-        // every PV of this key tile has read its operands: buffer free
-        if (elect_one()) umma_commit(&kv_empty[buf]);
-        __syncwarp();
-        if (i + 2 < ntl) {
-          const int nb2 = (i + 2) % NB;
-          if (!wait(&kv_full[nb2], (uint32_t)(((i + 2) / NB) & 1))) break;
-#pragma unroll
-          for (int j = 0; j < NQ; ++j) {
-            if (j >= nqt) break;
-            if (!wait(&pv_done[j], (uint32_t)(i & 1))) { go = false; break; }
-            issue_s(j, nb2, sb);
-          }
-          if (!go) break;
-        }
-      }
+      // every PV of this key tile has read its operands (and every S of it ended
+      // before its softmax): buffer free
+      if (go && elect_one()) umma_commit(&kv_empty[i % NB]);
+      __syncwarp();
+      return go;
+    };
+    bool go = true;
+    if constexpr (FEW) {
+      for (int i = 0; go && i < 2 && i < ntl; ++i) go = scores(i);
+      for (int i = 0; go && i < ntl; ++i) go = values(i) && (i + 2 >= ntl || scores(i + 2));
+    } else if (warp == RL::MMA_S) {
+      for (int i = 0; go && i < ntl; ++i) go = scores(i);
+    } else {
+      for (int i = 0; go && i < ntl; ++i) go = values(i);
     }
-    // everything issued completes before the epilogue and the exit
-    if (elect_one()) umma_commit(o_fin);
+    // everything that this warp issued completes before the epilogue and the exit
+    uint64_t* fin = warp == RL::MMA_PV ? o_fin : s_fin;
+    if (elect_one()) umma_commit(fin);
     __syncwarp();
-    (void)mbar_wait(o_fin, 0u);
+    (void)mbar_wait(fin, 0u);
   } else if (warp < 4 * nqt) {
     // ---- softmax of query tile j: one thread per row (its tensor-memory lane)
     const int j = warp >> 2;
@@ -888,7 +895,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
       // tile's S, and the PV that last read P' there completed before that S
       // was issued.
       if (i > 0 && __any_sync(0xffffffffu, al != 1.f)) {
-        const bool w2 = __all_sync(0xffffffffu, mbar_wait(&pv_done[j], (uint32_t)((i - 1) & 1)));
+        const bool w2 = __all_sync(0xffffffffu, mbar_wait(&pv_done[2 * j + ((i - 1) & 1)], (uint32_t)(((i - 1) >> 1) & 1)));
         if (!w2 && lane == 0) { *s_abort = 1; atomicOr(a.err, ERR_TIMEOUT); }
         if (!w2 || __any_sync(0xffffffffu, *s_abort)) return false;
         tc_fence_after();
