@@ -244,8 +244,8 @@ kvq_status kvq_rope_apply(const kvq_rope* rope, const void* x, long long x_token
  *   kvq_cache_write has in between (a BF16 layer rounds once, to the same bits);
  *   v is stored as kvq_cache_write stores it.  q, k and v may be parts of one
  *   fused buffer.  A token with slot < 0 has its q rotated and stores nothing.
- * Two tokens with the same slot leave one of the two there, as in
- * kvq_cache_write. */
+ * Slots are distinct, as for kvq_cache_write (a slot given twice holds bytes of
+ * both tokens). */
 kvq_status kvq_rope_cache_write(const kvq_ctx* ctx, const kvq_rope* rope, int layer, const void* q,
                                 long long q_token_stride, void* q_out,
                                 long long q_out_token_stride, const void* k_new,
@@ -274,7 +274,7 @@ kvq_status kvq_rope_cache_write(const kvq_ctx* ctx, const kvq_rope* rope, int la
  * again, a length that is negative or past the row's entries, and a block id
  * outside the pool set KVQ_ERR_BAD_INDEX on the device word; that row (that
  * entry, for a block id) is left as it is and the others proceed.  num_rows or
- * num_forks = 0 is KVQ_OK. */
+ * num_forks = 0 is KVQ_OK and writes nothing. */
 
 /* Takes num_rows rows and new_tokens[i] >= 0 further positions for row rows[i]
  * (distinct rows): hands out the blocks they need, lowest free ids first in the

@@ -13,31 +13,34 @@
 // and streams the keys of both in tiles of 64 positions.  At head_dim 256 a
 // CTA owns one query tile (its O takes 256 tensor-memory columns) and keeps
 // Q in tensor memory, the A operand of S; the roles below then have one
-// softmax warpgroup and the other warps move down by four.  Roles (14 warps):
+// softmax warpgroup and the other warps move down by four.  Roles (15 warps):
 //  * warp 12, producer: 2-D TMA copies of the key tile's K and V page tiles
 //    (and 64-byte bulk copies of their dynamic scales) into a ring of raw
-//    stages; lane s takes page tile s.
-//  * warps 8-11, converters: raw codes -> f16 in the tensor cores' layout,
-//    K as 64 rows of D (K-major, 128-byte swizzle) and V transposed (D rows
-//    of 64 keys, by a byte transpose in registers); K and V scales (zero for a
-//    key outside the CTA's range or on a page that was not fetched) and the
-//    tile's largest V-scale exponent.  Three operand buffers.  BF16 layers:
+//    stages, issued by an elected lane; the block ids of 32 page tiles are
+//    loaded at once, a round ahead.
+//  * warps 8-11, converters: raw codes -> f16, K and V alike as 64 rows (keys)
+//    of D in 64-d blocks of 128-byte rows with the 128-byte swizzle: the
+//    K-major operand of S and the MN-major operand of PV, so nothing is
+//    transposed; K and V scales (zero for a key outside the CTA's range or on a
+//    page that was not fetched) and the tile's largest V-scale exponent.  Three
+//    operand buffers.  BF16 layers:
 //    K stays bf16 (S is a bf16 MMA; at head_dim 128 the producer copies it
 //    straight into its operand buffer), and the converters give each V row
 //    the power-of-two V scale that maps its largest exponent to 2^14,
 //    converting it to f16 exactly; the rest then runs as for dynamic scales.
-//  * warp 13, MMA issuer (one thread): S_j = Q_j K^T (M 128, N 64) into
-//    tensor memory for each query tile j, and O_j += P'_j V with P'_j read
+//  * warps 13 and 14, MMA issuers (one thread each): S_j = Q_j K^T (M 128, N 64)
+//    into tensor memory for each query tile j, and O_j += P'_j V with P'_j read
 //    from tensor memory, every term of its f16 hi + lo split.  Each query
 //    tile has two S/P' buffers (key tile t uses buffer t & 1; P' replaces S
-//    there).  Order per key tile t: PV_0(t), PV_1(t), then S_0(t+2) and
-//    S_1(t+2) once the PV that last read each buffer has completed, so a
-//    softmax warpgroup finds the scores of its next tile ready and the
-//    tensor cores work on one query tile while the other's softmax runs.
+//    there): S_j(t+2) is issued once the PV that last read its buffer, PV_j(t),
+//    has completed, so a softmax warpgroup finds the scores of its next tile
+//    ready and the tensor cores work on one query tile while the other's
+//    softmax runs.
 //  * warps 0-3 and 4-7, softmax of query tile 0 and 1: one thread per row
 //    (its tensor-memory lane) loads the row's 64 scores, applies the K scale
-//    and masks, keeps a lazily moved reference max (moved only when a tile's
-//    max exceeds it by more than 8 in log2 units), rescales the row of O in tensor memory
+//    and masks (pairs of fp32 per instruction), keeps a lazily moved reference
+//    max (moved only when a tile's max exceeds it by more than 8 in log2 units),
+//    rescales the row of O in tensor memory
 //    when it moves, and stores P' = p x v_scale x 2^k (f16 hi + lo) over the
 //    scores it has read.
 // Tensor memory: two S/P' buffers per query tile (64 columns each), O_0, O_1
@@ -45,6 +48,10 @@
 // Every wait is bounded; a wait that runs out flags TIMEOUT and sets a
 // shared abort flag that ends every role's loop, the work already issued is
 // waited for (bounded again), and tensor memory is freed before the CTA exits.
+//
+// Measured (FP8 per-token-head, 1,024 new tokens a sequence after 3,072): 604
+// TFLOP/s at head_dim 128 (0.31 of the bf16 peak), 427 at 64; 676 at 256 (8,192
+// new tokens after 8,192).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
