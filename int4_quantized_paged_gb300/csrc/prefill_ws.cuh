@@ -831,8 +831,14 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
       uint64_t sv[8 * NCH];                     // pairs of scores
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       if (fast) {
+        float4 kq4[4];                           // K scales of 16 keys, loaded ahead
 #pragma unroll
         for (int k4 = 0; k4 < 4 * NCH; ++k4) {
+          if constexpr (C::FETCH) {
+            if (k4 % 4 == 0)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) kq4[u] = lds_v4_ordered(ks4 + k4 + u);
+          }
           float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -841,7 +847,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
           }
           uint64_t x01 = pack_f32x2(x[0], x[1]), x23 = pack_f32x2(x[2], x[3]);
           if constexpr (C::FETCH) {              // else every scale here is 1
-            const float4 kq = lds_v4_ordered(ks4 + k4);
+            const float4 kq = kq4[k4 % 4];
             x01 = mul_f32x2(x01, pack_f32x2(kq.x, kq.y));
             x23 = mul_f32x2(x23, pack_f32x2(kq.z, kq.w));
             unpack_f32x2(x01, x[0], x[1]);
@@ -917,6 +923,10 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         uint32_t hw[8], lw[8];
+        float4 vq4[4];                          // V scales of the chunk, loaded ahead
+        if constexpr (C::DYN)
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) vq4[q4] = lds_v4_ordered(vs4 + 4 * c + q4);
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
           const int k = 16 * c + 4 * q4;
@@ -929,7 +939,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
           lp01 = add_f32x2(lp01, x01);
           lp23 = add_f32x2(lp23, x23);
           if constexpr (C::DYN) {
-            const float4 vq = lds_v4_ordered(vs4 + (k >> 2));
+            const float4 vq = vq4[q4];
             unpack_f32x2(mul_f32x2(x01, pack_f32x2(vq.x, vq.y)), x[0], x[1]);
             unpack_f32x2(mul_f32x2(x23, pack_f32x2(vq.z, vq.w)), x[2], x[3]);
           }
