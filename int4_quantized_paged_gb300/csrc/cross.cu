@@ -21,8 +21,8 @@
 //    the tile two or four times, each copy with its share of a key tile's keys.
 //
 // What bounds it.  Many queries: 4 D flops per row and key on the tensor cores; 8 x
-// 900-1,024 queries x 3,000-4,096 states, 32 heads of 128, FP8: 422 us, 1,061
-// TFLOP/s (0.54 of the cuBLAS bf16 rate); a softmax thread's chain of dependent
+// 900-1,024 queries x 3,000-4,096 states, 32 heads of 128, FP8: 413 us, 1,084
+// TFLOP/s (0.56 of the cuBLAS bf16 rate); a softmax thread's chain of dependent
 // steps takes about 1,950 cycles a key tile, the MMAs of the two query tiles
 // about 1,300 (those of S read Q from shared memory again for every 64 keys).
 // Few queries: the pages' bytes; 8 x 1-5 queries x 20,000-32,768 states, 64 heads:

@@ -49,8 +49,8 @@
 // shared abort flag that ends every role's loop, the work already issued is
 // waited for (bounded again), and tensor memory is freed before the CTA exits.
 //
-// Measured (FP8 per-token-head, 1,024 new tokens a sequence after 3,072): 604
-// TFLOP/s at head_dim 128 (0.31 of the bf16 peak), 427 at 64; 676 at 256 (8,192
+// Measured (FP8 per-token-head, 1,024 new tokens a sequence at the end of
+// contexts of 4,096): 604 TFLOP/s at head_dim 128 (0.31 of the bf16 peak), 427 at 64; 676 at 256 (8,192
 // new tokens after 8,192).
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -23,8 +23,8 @@ constexpr int WS_CONV = 4;                          // warps of a converter grou
 constexpr int WROWS = 128;                          // rows per query tile (the MMA's M)
 
 // A 16-byte shared-memory load that stays after the tensor-memory stores
-// issued before it (both are volatile asm): the softmax reads a chunk's V
-// scales just before it uses them, instead of the compiler hoisting all
+// issued before it (both are volatile asm): the softmax reads the
+// scales of 16 keys ahead of their use, instead of the compiler hoisting all
 // sixteen loads of a tile to its start, where their 64 registers pushed the
 // thread past its 128-register share and spilled.
 __device__ __forceinline__ float4 lds_v4_ordered(const float4* p) {
@@ -54,7 +54,7 @@ __device__ __forceinline__ void store_row_f32(float* row, const float (&v)[32]) 
 // whose O needs 256 tensor-memory columns), a softmax warpgroup per query
 // tile, then the converters, the producer and two MMA issuers, of S and of PV
 // (FEW: one of both).
-// FEW (at most 128 rows): one query tile at every head_dim, and two converter
+// FEW (at most 128 rows): one query tile, built at head_dim 64 and 128, and two converter
 // groups that take key tiles in turn.  With one query tile a key tile's
 // conversion (1,500 cycles by one group) is a longer step than its MMAs, so the
 // second softmax warpgroup's place goes to a second converter.
@@ -127,8 +127,8 @@ struct WCfg {
   // Tensor-memory columns.  S/P' buffer b of query tile j: S (fp32, 64
   // columns), then P' (f16 hi in the first 32 columns, lo in the next 32) in
   // its place.  Two query tiles: S/P' at 64 (2 j + b), O_j at 256 + D j.  One
-  // query tile (D 256): O at 0, S/P' at 256 + 64 b, Q (f16, D / 2 columns) at
-  // 384.
+  // query tile (D 256, FEW): O at 0, S/P' at 256 + 64 b, Q (f16, D / 2 columns)
+  // at 384.
   __host__ __device__ static constexpr int scol(int j, int b) { return NQ == 2 ? 64 * (2 * j + b) : 256 + 64 * b; }
   __host__ __device__ static constexpr int ocol(int j) { return NQ == 2 ? 256 + D * j : 0; }
   static constexpr int QCOL = 384;
@@ -297,9 +297,10 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  // ---- queries: row R = 128 j + h * QP + i of query tile j -> query index
-  // qbase + j * QP + i, head g*G + h, prescaled by a power of two so the bf16
-  // values are exact in f16 (BF16 layers: the bf16 values as they are).
+  // ---- queries: row R = 128 j + r of query tile j -> query index
+  // qbase + j * QP + row_query(r), head g * heads + row_head(r), prescaled
+  // by a power of two so the bf16 values are exact in f16 (BF16 layers: the bf16
+  // values as they are).
   float ks_static = 1.f;
   if constexpr (MODE == FP8_PER_TENSOR) ks_static = a.k_scale[0];
   if constexpr (MODE == FP8_PER_HEAD) ks_static = a.k_scale[g];
@@ -1049,18 +1050,19 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
         for (int c0 = 0; c0 < D; c0 += 32) {
           float v[32];
           tmem_ld32(tO + c0, v);
-          if (pA < 0) continue;
+          if (pA >= 0) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= w0;
-          if constexpr (FEW) {
-            for (int c = 1; c < copies; ++c)
+            for (int e = 0; e < 32; ++e) v[e] *= w0;
+            if constexpr (FEW) {
+              for (int c = 1; c < copies; ++c)
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                v[e] = fmaf(c == 1 ? wc[1] : (c == 2 ? wc[2] : wc[3]),
-                            xo[(c0 + e) * WROWS + r + c * copy_rows], v[e]);
+                for (int e = 0; e < 32; ++e)
+                  v[e] = fmaf(c == 1 ? wc[1] : (c == 2 ? wc[2] : wc[3]),
+                              xo[(c0 + e) * WROWS + r + c * copy_rows], v[e]);
+            }
+            if (whole) store_row_bf16(a.out_bf16 + orow * D + c0, v);
+            else store_row_f32(a.ws_o + prow * D + c0, v);
           }
-          if (whole) store_row_bf16(a.out_bf16 + orow * D + c0, v);
-          else store_row_f32(a.ws_o + prow * D + c0, v);
         }
       } else {
         float* dst = a.out + ((long long)(q0 + qbase + j * QP + ii) * a.Hq + g * heads + h) * D;
