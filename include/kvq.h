@@ -292,7 +292,7 @@ kvq_status kvq_rope_cache_write(const kvq_ctx* ctx, const kvq_rope* rope, int la
  * row i need more blocks than are free, row i is refused if it needs any
  * (KVQ_ERR_NO_BLOCKS on the device word); when they have more than max_tokens
  * tokens it is refused too (KVQ_ERR_BAD_INDEX).  A refused row keeps its length
- * and table.  num_rows <= 4096; max_tokens < 2^31. */
+ * and table.  num_rows <= 4096; max_tokens < 2^31 - 1. */
 kvq_status kvq_extend_sequences(const kvq_ctx* ctx, const int* rows, const int* new_tokens,
                                 int num_rows, int* ref_count, int* block_table, int table_rows,
                                 int max_blocks_per_seq, int* context_lens, long long max_tokens,

@@ -253,7 +253,7 @@ kvq_status kvq_extend_sequences(const kvq_ctx* ctx, const int* rows, const int* 
                                 int max_blocks_per_seq, int* context_lens, long long max_tokens,
                                 int* query_start, long long* positions, long long* slot_mapping,
                                 int* copies, void* stream) {
-  if (!ctx || num_rows < 0 || max_tokens < 0 || max_tokens >= (1LL << 31))
+  if (!ctx || num_rows < 0 || max_tokens < 0 || max_tokens >= (1LL << 31) - 1)
     return KVQ_ERR_INVALID_ARG;
   if (num_rows == 0) return KVQ_OK;
   kvq_status st =

@@ -58,7 +58,8 @@ def _extend(ctx, rows=T(OK, 4), new=OK, ref=OK, table=T(OK, 8, 16), lens=OK, qs=
     ("INVALID_ARG", dict(new=None)), ("INVALID_ARG", dict(ref=None)), ("INVALID_ARG", dict(lens=None)),
     ("INVALID_ARG", dict(qs=None)), ("INVALID_ARG", dict(pos=None)), ("INVALID_ARG", dict(slots=None)),
     ("INVALID_ARG", dict(copies=None)), ("INVALID_ARG", dict(max_tokens=-1)),
-    ("INVALID_ARG", dict(max_tokens=1 << 31)), ("INVALID_ARG", dict(table=T(OK, 8, 1 << 27))),
+    ("INVALID_ARG", dict(max_tokens=1 << 31)), ("INVALID_ARG", dict(max_tokens=(1 << 31) - 1)),
+    ("INVALID_ARG", dict(table=T(OK, 8, 1 << 27))),
     ("UNSUPPORTED", dict(rows=T(OK, 4097))),
     ("ALIGNMENT", dict(rows=T(OK + 2, 4))), ("ALIGNMENT", dict(table=T(OK + 1, 8, 16))),
     ("ALIGNMENT", dict(pos=OK + 4)), ("ALIGNMENT", dict(slots=OK + 4)), ("ALIGNMENT", dict(copies=OK + 2)),
