@@ -22,6 +22,7 @@
  *  - Pointers named *_cache, q, out, k_new, v_new, slot_mapping, block_table,
  *    context_lens, workspace and the scale arrays are DEVICE pointers owned by
  *    the caller; the library never allocates, frees or retains them.
+ *  - Streams and pointers belong to the current device of the calling thread.
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  Device work is enqueued asynchronously on it; a call returns
  *    once the work is enqueued.
@@ -395,7 +396,8 @@ size_t kvq_decode_workspace_size(const kvq_ctx* ctx, int layer, int batch, int m
  * num_workers: worker warps (see kvq_decode_plan); 0 = the plan's choice.
  *   With more than one worker, partials go to `workspace` (16-byte aligned,
  *   kvq_decode_plan gives its size); its contents need no initialisation.
- * Scale pointers as for kvq_cache_write. */
+ * Scale pointers as for kvq_cache_write; dynamic scale buffers are 16-byte
+ * aligned (they are fetched by bulk copies). */
 kvq_status kvq_decode_attention(const kvq_ctx* ctx, int layer, const void* q,
                                 const void* k_cache, const void* v_cache, const float* k_scale,
                                 const float* v_scale, const float* k_cache_scale,

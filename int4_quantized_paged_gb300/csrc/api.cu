@@ -261,7 +261,8 @@ kvq_status decode_impl(const kvq_ctx* ctx, int layer, const void* q, const float
     return KVQ_ERR_INVALID_ARG;
   if (is_dynamic(mode)) {
     if (!k_cache_scale || !v_cache_scale) return KVQ_ERR_INVALID_ARG;
-    if (!aligned4(k_cache_scale) || !aligned4(v_cache_scale)) return KVQ_ERR_ALIGNMENT;
+    // the kernels fetch 16 scales at a time by bulk copies
+    if (!aligned16(k_cache_scale) || !aligned16(v_cache_scale)) return KVQ_ERR_ALIGNMENT;
   }
   if (q_scale) {
     if (q_scale_count != 1 && q_scale_count != c.num_q_heads) return KVQ_ERR_INVALID_ARG;
@@ -391,7 +392,8 @@ kvq_status kvq_prefill_attention(const kvq_ctx* ctx, int layer, const void* q,
     return KVQ_ERR_INVALID_ARG;
   if (is_dynamic(mode)) {
     if (!k_cache_scale || !v_cache_scale) return KVQ_ERR_INVALID_ARG;
-    if (!aligned4(k_cache_scale) || !aligned4(v_cache_scale)) return KVQ_ERR_ALIGNMENT;
+    // the kernels fetch 16 scales at a time by bulk copies
+    if (!aligned16(k_cache_scale) || !aligned16(v_cache_scale)) return KVQ_ERR_ALIGNMENT;
   }
   const int G = c.num_q_heads / c.num_kv_heads;
   const long long qtiles = ((long long)max_query_len * G + kvq::prefill_rows_per_cta() - 1) /
