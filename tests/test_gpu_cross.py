@@ -201,6 +201,46 @@ def test_shared_states_and_graph():
     c.check()
 
 
+@pytest.mark.parametrize("splits", [2, 64, 1024])
+def test_more_splits_than_key_tiles(splits):
+    c = Case(4, 128, 8, 2, [500, 3, 130], [2, 7, 40], seed=15)
+    c.run(splits)
+    c.check()
+
+
+@pytest.mark.parametrize("mode, D, Hkv", [(3, 64, 1), (0, 128, 1), (2, 256, 3)])
+def test_many_sequences(mode, D, Hkv):
+    lens = [(37 * b) % 211 for b in range(300)]
+    c = Case(mode, D, 2 * Hkv, Hkv, lens, [(5 * b) % 4 for b in range(300)], bs=32, seed=16)
+    c.run()
+    c.check()
+    c.out.fill_(7.0)
+    c.run(2)
+    c.check()
+
+
+def test_rows_at_the_forms_borders():
+    """Queries x heads of 32, 33, 64, 65, 128 and 129: copies of the rows, idle warps, two tiles."""
+    for G, ns in ((8, (4, 8, 16, 17)), (1, (32, 33, 64, 65, 128, 129, 257))):
+        for n in ns:
+            c = Case(3, 64, G, 1, [700], [n], seed=n)
+            c.run()
+            c.check()
+
+
+def test_two_streams_at_once():
+    c = [Case(m, 128, 16, 2, [6000, 900], [3, 50], seed=17 + m) for m in (3, 0)]
+    streams = [torch.cuda.Stream() for _ in c]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for x, s in zip(c, streams):
+            with torch.cuda.stream(s):
+                x.run()
+    torch.cuda.synchronize()
+    for x in c:
+        x.check()
+
+
 def test_repeats_are_bit_equal():
     for mode in MODES:
         c = Case(mode, 128, 16, 2, [5000, 77], [5, 60], seed=14)
