@@ -31,6 +31,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "kvq_internal.h"
 #include "quantize.cuh"
 
@@ -66,15 +68,17 @@ __device__ __forceinline__ void rotate(float* x, const float* c, const float* s)
   }
 }
 
+// Vectors a lane has in flight.  Measured, 32,768 tokens x 80 heads of 128: 2: 217 us,
+// 3: 202, 4: 192 (99 % of the copy rate), 5: 191; 2,053 x 32 heads of 256: 2: 17.2,
+// 4: 18.2 (a vector takes 16 lanes, and registers end the occupancy).
+__host__ __device__ constexpr int in_flight(int D) { return D == 256 ? 2 : 4; }
+
 template <int MODE, int D, int LAYOUT>
 __global__ void __launch_bounds__(RWARPS * 32)
     rope_kernel(const RopeArgs a, const __grid_constant__ RopeTable tab) {
   constexpr int LPV = D / 16;                  // lanes per vector
   constexpr int GP = 32 / LPV;                 // vectors a warp holds at once
-  // and in flight per lane.  Measured, 32,768 tokens x 80 heads of 128: 2: 213 us,
-  // 3: 204, 4: 192 (99 % of the copy rate), 5: 191; 2,053 x 32 heads of 256: 2: 17.2,
-  // 4: 18.2 (a vector takes 16 lanes, and registers end the occupancy)
-  constexpr int U = D == 256 ? 2 : 4;
+  constexpr int U = in_flight(D);              // and has in flight per lane
   constexpr int NP = D / 64;                   // pairs a lane computes the angle of
   __shared__ __align__(16) float2 cs_all[RWARPS][D / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -107,6 +111,22 @@ __global__ void __launch_bounds__(RWARPS * 32)
     const long long slot = w.slots ? w.slots[t] : -1;
     const bool store = slot >= 0 && slot < cells;
     if (slot >= cells && v0 == 0 && lane == 0) atomicOr(w.err, ERR_BAD_INDEX);
+    uint4 r0[U], r1[U];
+    // the group's next vectors (the whole group agrees on `v`)
+    auto load = [&](int v) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int vv = v + GP * u;
+        if (vv >= v1 || (vv >= a.Hq && !store)) continue;
+        const uint16_t* src =
+            vv < a.Hq ? a.q + (long long)t * a.q_stride + (long long)vv * D
+                      : (vv < hk ? w.k_new + (long long)t * w.token_stride + (long long)(vv - a.Hq) * D
+                                 : w.v_new + (long long)t * w.token_stride + (long long)(vv - hk) * D);
+        r0[u] = reinterpret_cast<const uint4*>(src)[c0];
+        r1[u] = reinterpret_cast<const uint4*>(src)[c1];
+      }
+    };
+    load(v0 + gi);                             // in flight while the angles are computed
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int p = lane + 32 * i;
@@ -130,18 +150,7 @@ __global__ void __launch_bounds__(RWARPS * 32)
     const unsigned blk = (unsigned)((store ? slot : 0) >> w.bs_shift);
     const unsigned off = (unsigned)(store ? slot : 0) & (unsigned)(w.bs - 1);
     for (int v = v0 + gi; v < v1; v += GP * U) {
-      uint4 r0[U], r1[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int vv = v + GP * u;
-        if (vv >= v1 || (vv >= a.Hq && !store)) continue;
-        const uint16_t* src =
-            vv < a.Hq ? a.q + (long long)t * a.q_stride + (long long)vv * D
-                      : (vv < hk ? w.k_new + (long long)t * w.token_stride + (long long)(vv - a.Hq) * D
-                                 : w.v_new + (long long)t * w.token_stride + (long long)(vv - hk) * D);
-        r0[u] = reinterpret_cast<const uint4*>(src)[c0];
-        r1[u] = reinterpret_cast<const uint4*>(src)[c1];
-      }
+      if (v != v0 + gi) load(v);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int vv = v + GP * u;
@@ -199,25 +208,36 @@ __global__ void __launch_bounds__(RWARPS * 32)
 
 template <int MODE, int D, int LAYOUT>
 cudaError_t launch_l(RopeArgs& a, const RopeTable& tab, cudaStream_t st) {
-  // Work per warp: a whole token once the tokens alone give every SM 32 warps;
-  // fewer tokens are cut into slices of their vectors (GP at least, so that no
-  // lane idles), down to one pass per warp, which is what a decode step gets.
+  // Work per warp: a token, or a slice of its vectors (GP at least, so that no lane
+  // idles).  A warp's item costs its rounds of loads and about one more for the
+  // angles; the cut that takes the fewest of them over the waves of resident warps
+  // wins, the finer one where two cost the same (a decode step: one round per warp).
+  // Measured, 2,053 tokens x 32 heads of 256, one slice (a wave): 17.1 us, two or
+  // three (a second, partly filled wave): 18.8; 8,192 x 80 heads of 64: 30.4 and 32.3.
   constexpr int GP = 32 / (D / 16);
   const int nv = a.Hq + 2 * a.w.Hkv;
-  const long long want = (long long)sm_count() * 32;
-  int slices = (int)((want + a.w.T - 1) / a.w.T);
-  const int most = (nv + GP - 1) / GP;
-  if (slices > most) slices = most;
-  if (slices < 1) slices = 1;
-  int per = (nv + slices - 1) / slices;
-  per = (per + GP - 1) / GP * GP;
+  constexpr int ROUND = GP * in_flight(D);                     // vectors a warp loads at once
+  const long long warps = (long long)sm_count() * 16;          // resident (97-117 registers)
+  // more than two waves of slices of a vector group never win
+  const int most = (int)std::min((long long)(nv + GP - 1) / GP, 2 * warps / a.w.T + 1);
+  int per = 0;
+  long long best = 0;
+  for (int s = most; s >= 1; --s) {
+    const int p = ((nv + s - 1) / s + GP - 1) / GP * GP;
+    const long long items = a.w.T * ((nv + p - 1) / p);
+    const long long cost = (items + warps - 1) / warps * ((p + ROUND - 1) / ROUND + 1);
+    if (per == 0 || cost < best) {
+      best = cost;
+      per = p;
+    }
+  }
   a.per_slice = per;
   a.slices = (nv + per - 1) / per;
   const long long items = a.w.T * a.slices;
   if (items >= (1LL << 31)) return cudaErrorInvalidValue;
   long long grid = (items + RWARPS - 1) / RWARPS;
-  // resident CTAs and no more: a warp then carries its frequencies over several
-  // items (16 or 32 per SM measured 1 to 4 % slower)
+  // two waves of CTAs and no more: a warp then carries its frequencies over several
+  // items (16 or 64 per SM measured 1 to 4 % slower)
   const long long cap = (long long)sm_count() * 8;
   if (grid > cap) grid = cap;
   rope_kernel<MODE, D, LAYOUT><<<(unsigned)grid, RWARPS * 32, 0, st>>>(a, tab);
