@@ -21,9 +21,9 @@
 //    the tile two or four times, each copy with its share of a key tile's keys.
 //
 // What bounds it.  Many queries: 4 D flops per row and key on the tensor cores; 8 x
-// 900-1,024 queries x 3,000-4,096 states, 32 heads of 128, FP8: 413 us, 1,084
-// TFLOP/s (0.56 of the cuBLAS bf16 rate); a softmax thread's chain of dependent
-// steps takes about 1,950 cycles a key tile, the MMAs of the two query tiles
+// 900-1,024 queries x 3,000-4,096 states, 32 heads of 128, FP8: 398 us, 1,124
+// TFLOP/s (0.58 of the cuBLAS bf16 rate); a softmax thread's chain of dependent
+// steps takes about 1,880 cycles a key tile, the MMAs of the two query tiles
 // about 1,300 (those of S read Q from shared memory again for every 64 keys).
 // Few queries: the pages' bytes; 8 x 1-5 queries x 20,000-32,768 states, 64 heads:
 // 136 us, 3.2 TB/s (0.48); a key tile's 16 KB pass an SM in 770 cycles at the copy
@@ -169,12 +169,12 @@ cudaError_t claunch(const PrefillArgs& pa, cudaStream_t st) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   auto kern = prefill_ws_kernel<MODE, D, 0, true, FEW>;
   if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    const cudaError_t e = ws_prepare<WRoles<MODE, D, FEW>>(kern, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const long long grid = (long long)pa.qtiles * pa.splits * a.B * a.Hkv;
-  kern<<<(unsigned)grid, WRoles<D, FEW>::THREADS, C::SMEM, st>>>(pa, km, vm);
+  kern<<<(unsigned)grid, WRoles<MODE, D, FEW>::THREADS, C::SMEM, st>>>(pa, km, vm);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || pa.splits <= 1) return e;
   const long long items = (long long)a.B * pa.max_query * a.Hq;
@@ -210,7 +210,7 @@ cudaError_t claunch_d(int D, const PrefillArgs& pa, cudaStream_t st) {
 }  // namespace
 
 int cross_query_tile(int D, int G) {
-  return (D == 256 ? WRoles<256, false>::NQ : WRoles<128, false>::NQ) * (WROWS / G);
+  return (D == 256 ? WRoles<BF16, 256, false>::NQ : WRoles<BF16, 128, false>::NQ) * (WROWS / G);
 }
 
 cudaError_t launch_cross(int mode, int D, int G, const DecodeArgs& a, const int* query_start,

@@ -13,7 +13,9 @@
 // and streams the keys of both in tiles of 64 positions.  At head_dim 256 a
 // CTA owns one query tile (its O takes 256 tensor-memory columns) and keeps
 // Q in tensor memory, the A operand of S; the roles below then have one
-// softmax warpgroup and the other warps move down by four.  Roles (15 warps):
+// softmax warpgroup and the other warps move down by four.  Roles (15 warps and one
+// that completes the last warpgroup; the softmax warpgroups take registers that the
+// others give up):
 //  * warp 12, producer: 2-D TMA copies of the key tile's K and V page tiles
 //    (and 64-byte bulk copies of their dynamic scales) into a ring of raw
 //    stages, issued by an elected lane; the block ids of 32 page tiles are
@@ -50,8 +52,8 @@
 // waited for (bounded again), and tensor memory is freed before the CTA exits.
 //
 // Measured (FP8 per-token-head, 1,024 new tokens a sequence at the end of
-// contexts of 4,096): 604 TFLOP/s at head_dim 128 (0.31 of the bf16 peak), 427 at 64; 676 at 256 (8,192
-// new tokens after 8,192).
+// contexts of 4,096): 621 TFLOP/s at head_dim 128 (0.32 of the bf16 peak), 430 at 64;
+// 676 at 256 (8,192 new tokens after 8,192).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -117,16 +119,16 @@ cudaError_t wslaunch3(const PrefillArgs& pa0, int max_query_len, cudaStream_t st
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   auto kern = prefill_ws_kernel<MODE, D, G>;
   if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    const cudaError_t e = ws_prepare<WRoles<MODE, D, false>>(kern, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   PrefillArgs pa = pa0;
-  const int qp2 = WRoles<D, false>::NQ * (WROWS / G);      // query positions per CTA
+  const int qp2 = WRoles<MODE, D, false>::NQ * (WROWS / G);      // query positions per CTA
   pa.qtiles = (max_query_len + qp2 - 1) / qp2;
   const long long grid = (long long)pa.qtiles * a.B * a.Hkv;
   if (grid <= 0) return cudaSuccess;
-  kern<<<(unsigned)grid, WRoles<D, false>::THREADS, C::SMEM, st>>>(pa, km, vm);
+  kern<<<(unsigned)grid, WRoles<MODE, D, false>::THREADS, C::SMEM, st>>>(pa, km, vm);
   return cudaGetLastError();
 }
 

@@ -50,6 +50,16 @@ __device__ __forceinline__ void store_row_f32(float* row, const float (&v)[32]) 
   for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
 }
 
+// A warpgroup's registers a thread, from here on.
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Warp roles: NQ query tiles per CTA (two at head_dim 64 and 128; one at 256,
 // whose O needs 256 tensor-memory columns), a softmax warpgroup per query
 // tile, then the converters, the producer and two MMA issuers, of S and of PV
@@ -58,7 +68,7 @@ __device__ __forceinline__ void store_row_f32(float* row, const float (&v)[32]) 
 // groups that take key tiles in turn.  With one query tile a key tile's
 // conversion (1,500 cycles by one group) is a longer step than its MMAs, so the
 // second softmax warpgroup's place goes to a second converter.
-template <int D, bool FEW>
+template <int MODE, int D, bool FEW>
 struct WRoles {
   static constexpr int NQ = (D == 256 || FEW) ? 1 : 2;
   static constexpr int CG = FEW ? 2 : 1;             // converter groups
@@ -66,7 +76,21 @@ struct WRoles {
   static constexpr int PROD = SOFT + CG * WS_CONV;   // producer warp
   static constexpr int MMA_S = PROD + 1;             // warp that issues S
   static constexpr int MMA_PV = FEW ? MMA_S : PROD + 2;   // and the one that issues PV
-  static constexpr int THREADS = (MMA_PV + 1) * 32;  // 480, 448 or 352
+  // Two query tiles and a scale per key: four warpgroups (warp 15 only completes
+  // the fourth), whose registers move to the softmax: its 64 scores, the scales
+  // ahead and its sums spilled in an even share of 128, and the other roles need
+  // fewer.  Cross attention of 8 x 900-1,024 queries to 3,000-4,096 states, 32 heads
+  // of 128: 412 -> 398 us; prefill per token and head 603 -> 621 TFLOP/s, INT4 583 ->
+  // 588; without scales per key the softmax has room, and the same split measured
+  // 727 -> 712 (per head) and 574 -> 568 (BF16).
+  // The shares add up to what the block is launched with, or the softmax would
+  // wait for registers that nobody gives up.
+  static constexpr bool SPLIT_REGS =
+      NQ == 2 && (MODE == FP8_PER_TOKEN_HEAD || MODE == INT4_PER_TOKEN_HEAD);
+  static constexpr int THREADS = SPLIT_REGS ? 512 : (MMA_PV + 1) * 32;   // 512, 480, 448 or 352
+  static constexpr int REGS = 128;                   // a thread at launch (SPLIT_REGS)
+  static constexpr int REGS_SOFT = 168, REGS_CONV = 112, REGS_REST = 64;
+  static_assert(!SPLIT_REGS || 2 * REGS_SOFT + REGS_CONV + REGS_REST == 4 * REGS, "register shares");
 };
 constexpr int WKT = 64;                             // keys per tile
 constexpr int WKP = 6;                              // P' = p v_scale 2^(WKP - vexp) < 2^15 (p <= 2^8)
@@ -102,7 +126,7 @@ struct WCfg {
   static constexpr int VOFF = KDIRECT ? 0 : SUB * TBP;      // V page tiles in a raw stage
   static constexpr int SCB = FETCH ? 2 * SUB * 64 : 0;
   static constexpr int RAWS = (RAW + SCB + 1023) / 1024 * 1024;
-  static constexpr int NQ = WRoles<D, FEW>::NQ;
+  static constexpr int NQ = WRoles<MODE, D, FEW>::NQ;
   static constexpr int QB = WROWS * D * 2;                  // one query tile: D/64 blocks of 128 x 128 B
   // queries in shared memory (two query tiles); with one query tile they live
   // in tensor memory instead, the A operand of S
@@ -142,11 +166,11 @@ struct WCfg {
 // CROSS true: attention to all positions of the sequence (no mask), 2^g_shift
 // query heads per KV head, bf16 output, the keys cut into splits; FEW as above.
 template <int MODE, int D, int G, bool CROSS = false, bool FEW = false>
-__global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
+__global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
     prefill_ws_kernel(const PrefillArgs pa, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
   using C = WCfg<MODE, D, FEW>;
-  using RL = WRoles<D, FEW>;
+  using RL = WRoles<MODE, D, FEW>;
   constexpr int NQ = RL::NQ;
   const DecodeArgs& a = pa.d;
   constexpr int SUB = C::SUB;
@@ -445,6 +469,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
     // ids of 32 page tiles are loaded at once, one per lane and a round ahead, and
     // every copy is issued by an elected lane from warp-uniform operands (copies
     // issued by the page tiles' own lanes took a loop over the lanes each).
+    if constexpr (RL::SPLIT_REGS) give_registers<RL::REGS_REST>();
     int last[NR];                                  // tile index last issued into each stage
 #pragma unroll
     for (int s = 0; s < NR; ++s) last[s] = -1;
@@ -532,6 +557,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
         if (last[s] >= 0) (void)mbar_wait(&raw_full[s], (uint32_t)((last[s] / NR) & 1));
   } else if (warp >= RL::SOFT && warp < RL::PROD) {
     // ---- converters (groups of 128 threads, taking key tiles in turn)
+    if constexpr (RL::SPLIT_REGS) give_registers<RL::REGS_CONV>();
     const int cgrp = RL::CG == 1 ? 0 : (warp - RL::SOFT) / WS_CONV;
     const int ct_ = tid - (RL::SOFT + cgrp * WS_CONV) * 32;
     const int conv_bar = CONV_BAR + cgrp;
@@ -688,6 +714,7 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
     // tile held up the other tile's next scores, and its waits and issues alone
     // took 1,900 cycles of a key tile's 2,700.  With one query tile (FEW) there is
     // nothing to hold up, and a second polling warp costs more (134 -> 143 us).
+    if constexpr (RL::SPLIT_REGS) give_registers<RL::REGS_REST>();
     constexpr uint32_t IDS = mma_idesc<C::BFK>(WROWS, WKT);   // bf16 Q and K for BF16 layers
     constexpr uint32_t IDO = mma_idesc<false>(WROWS, D) | MMA_B_MN_MAJOR;
     auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
@@ -780,8 +807,12 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
     if (elect_one()) umma_commit(fin);
     __syncwarp();
     (void)mbar_wait(fin, 0u);
+  } else if (warp > RL::MMA_PV) {
+    // ---- completes the last warpgroup
+    if constexpr (RL::SPLIT_REGS) give_registers<RL::REGS_REST>();
   } else if (warp < 4 * nqt) {
     // ---- softmax of query tile j: one thread per row (its tensor-memory lane)
+    if constexpr (RL::SPLIT_REGS) take_registers<RL::REGS_SOFT>();
     const int j = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const int R = j * WROWS + r;
@@ -1089,6 +1120,18 @@ __global__ void __launch_bounds__(WRoles<D, FEW>::THREADS, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(C::TCOLS));
   }
+}
+
+// Once per kernel and device, before its first launch.
+template <class RL, class Kernel>
+cudaError_t ws_prepare(Kernel kern, int smem) {
+  if (RL::SPLIT_REGS) {                        // the shares fit what a launch gets
+    cudaFuncAttributes at;
+    const cudaError_t e = cudaFuncGetAttributes(&at, kern);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs < RL::REGS) return cudaErrorInvalidConfiguration;
+  }
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 }  // namespace
