@@ -122,8 +122,9 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # the handle alone: a torch Stream object costs more than a small launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # the handle alone: a torch Stream object costs more than a small launch, and
+        # torch.cuda.current_device() as much as the rest of this
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -250,7 +251,7 @@ def kvq_rope_apply(rope: Rope, x, positions, out, *, inverse: bool = False, x_to
                    num_heads: Optional[int] = None, stream=None):
     T = x.shape[0] if num_tokens is None else num_tokens
     H = x.shape[1] if num_heads is None else num_heads
-    _check(_lib.kvq_rope_apply(rope, _ptr(x), x_token_stride, _ptr(positions), T, H, _ptr(out),
+    _check(_lib.kvq_rope_apply(rope.handle, _ptr(x), x_token_stride, _ptr(positions), T, H, _ptr(out),
                                out_token_stride, int(inverse), _stream(stream)), "kvq_rope_apply")
 
 
@@ -262,7 +263,7 @@ def kvq_rope_cache_write(ctx: Context, rope: Rope, layer: int, q, q_out, k_new, 
     """kvq_cache_write of rotated keys; rotates q into q_out too (both None: keys only)."""
     T = k_new.shape[0] if num_tokens is None else num_tokens
     _check(_lib.kvq_rope_cache_write(
-        ctx, rope, layer, _ptr(q), q_token_stride, _ptr(q_out), q_out_token_stride, _ptr(k_new),
+        ctx.handle, rope.handle, layer, _ptr(q), q_token_stride, _ptr(q_out), q_out_token_stride, _ptr(k_new),
         _ptr(v_new), kv_token_stride, _ptr(positions), _ptr(slot_mapping), T, _ptr(k_scale),
         _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), _ptr(k_cache_scale), _ptr(v_cache_scale),
         _stream(stream)), "kvq_rope_cache_write")
@@ -274,14 +275,14 @@ def kvq_extend_sequences(ctx: Context, rows, new_tokens, ref_count, block_table,
     """Blocks, positions and slots for new_tokens[i] more tokens of row rows[i]."""
     n = positions.numel() if max_tokens is None else max_tokens
     _check(_lib.kvq_extend_sequences(
-        ctx, _ptr(rows), _ptr(new_tokens), rows.numel(), _ptr(ref_count), _ptr(block_table),
+        ctx.handle, _ptr(rows), _ptr(new_tokens), rows.numel(), _ptr(ref_count), _ptr(block_table),
         block_table.shape[0], block_table.shape[1], _ptr(context_lens), n, _ptr(query_start),
         _ptr(positions), _ptr(slot_mapping), _ptr(copies), _stream(stream)), "kvq_extend_sequences")
 
 
 def kvq_fork_sequences(ctx: Context, parents, children, ref_count, block_table, context_lens,
                        stream=None):
-    _check(_lib.kvq_fork_sequences(ctx, _ptr(parents), _ptr(children), parents.numel(),
+    _check(_lib.kvq_fork_sequences(ctx.handle, _ptr(parents), _ptr(children), parents.numel(),
                                    _ptr(ref_count), _ptr(block_table), block_table.shape[0],
                                    block_table.shape[1], _ptr(context_lens), _stream(stream)),
            "kvq_fork_sequences")
@@ -290,7 +291,7 @@ def kvq_fork_sequences(ctx: Context, parents, children, ref_count, block_table, 
 def kvq_truncate_sequences(ctx: Context, rows, keep_lens, ref_count, block_table, context_lens,
                            stream=None):
     """keep_lens None frees the rows."""
-    _check(_lib.kvq_truncate_sequences(ctx, _ptr(rows), _ptr(keep_lens), rows.numel(),
+    _check(_lib.kvq_truncate_sequences(ctx.handle, _ptr(rows), _ptr(keep_lens), rows.numel(),
                                        _ptr(ref_count), _ptr(block_table), block_table.shape[0],
                                        block_table.shape[1], _ptr(context_lens), _stream(stream)),
            "kvq_truncate_sequences")
@@ -299,7 +300,7 @@ def kvq_truncate_sequences(ctx: Context, rows, keep_lens, ref_count, block_table
 def kvq_compact_blocks(ctx: Context, ref_count, block_table, context_lens, moves, num_moves,
                        stream=None):
     """moves: int32 [num_blocks // 2, 2] (old, new); num_moves: int32 [1]."""
-    _check(_lib.kvq_compact_blocks(ctx, _ptr(ref_count), _ptr(block_table), block_table.shape[0],
+    _check(_lib.kvq_compact_blocks(ctx.handle, _ptr(ref_count), _ptr(block_table), block_table.shape[0],
                                    block_table.shape[1], _ptr(context_lens), _ptr(moves),
                                    _ptr(num_moves), _stream(stream)), "kvq_compact_blocks")
 
@@ -328,7 +329,7 @@ def kvq_copy_blocks(ctx: Context, pairs, layers: LayerPointers, *, num_pairs=Non
                     first_layer: int = 0, max_pairs: Optional[int] = None, stream=None):
     """Copies block pairs[i, 0] to pairs[i, 1] in every layer of `layers`."""
     n = pairs.shape[0] if max_pairs is None else max_pairs
-    _check(_lib.kvq_copy_blocks(ctx, first_layer, layers.num_layers, _ptr(pairs), n,
+    _check(_lib.kvq_copy_blocks(ctx.handle, first_layer, layers.num_layers, _ptr(pairs), n,
                                 _ptr(num_pairs), *layers.arrays, _stream(stream)),
            "kvq_copy_blocks")
 
@@ -446,7 +447,7 @@ def kvq_cross_plan(ctx: Context, layer: int, batch: int, max_query_len: int, max
                    num_splits: int = 0):
     """(splits, workspace bytes); max_query_len 0: one query per sequence."""
     s, w = i32(num_splits), sz()
-    _check(_lib.kvq_cross_plan(ctx, layer, batch, max_query_len, max_encoder_len, ctypes.byref(s),
+    _check(_lib.kvq_cross_plan(ctx.handle, layer, batch, max_query_len, max_encoder_len, ctypes.byref(s),
                                ctypes.byref(w)), "kvq_cross_plan")
     return s.value, w.value
 
@@ -464,7 +465,7 @@ def kvq_cross_attention(ctx: Context, layer: int, q, k_cache, v_cache, block_tab
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.kvq_cross_attention(
-        ctx, layer, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        ctx.handle, layer, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
         _ptr(k_cache_scale), _ptr(v_cache_scale), _ptr(block_table), mb, _ptr(query_start),
         _ptr(encoder_lens), B, max_query_len, max_encoder_len, _ptr(out), num_splits,
         _ptr(workspace), workspace_bytes, _stream(stream)), "kvq_cross_attention")
