@@ -497,7 +497,9 @@ kvq_status kvq_prefill_attention(const kvq_ctx* ctx, int layer, const void* q,
  * max_encoder_len: an upper bound of encoder_lens, used by the plan only; more
  *   than the table rows cover is KVQ_ERR_INVALID_ARG.
  * num_splits, workspace: from kvq_cross_plan with the same sizes; num_splits 0
- *   = the plan's choice.  The workspace (16-byte aligned) needs no
+ *   = the plan's choice.  With query_start NULL and max_query_len 1 the call takes
+ *   the worker warps that the plan of 0 chooses, and num_splits of them only where
+ *   the workspace is smaller than theirs.  The workspace (16-byte aligned) needs no
  *   initialisation; overlapping calls need one each.
  * Softmax and sums are fp32; the weight that meets a value is rounded to f16
  * (an eighth of the output's own rounding).  A layer with a window is
@@ -518,7 +520,8 @@ kvq_status kvq_cross_attention(const kvq_ctx* ctx, int layer, const void* q, con
  * *num_splits > 0 (at most 1024) requests a count, 0 asks for the plan's choice
  * (one split when the queries fill the SMs; for few queries, as many as do).
  * max_query_len 0 plans the form with query_start NULL (*num_splits then counts
- * worker warps, as in kvq_decode_plan). */
+ * worker warps, as in kvq_decode_plan).  The workspace of max_query_len 1 serves
+ * the call with query_start and the one without. */
 kvq_status kvq_cross_plan(const kvq_ctx* ctx, int layer, int batch, int max_query_len,
                           int max_encoder_len, int* num_splits, size_t* workspace_bytes);
 

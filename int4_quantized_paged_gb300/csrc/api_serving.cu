@@ -85,6 +85,29 @@ int plan_splits(long long base, int tiles) {
   return best;
 }
 
+// Splits (0 in: the plan's choice) and workspace bytes of a cross attention call
+// with query_start, or with max_query_len 0 of the one without.
+kvq_status plan_cross(const kvq_ctx* ctx, int layer, int batch, int max_query_len,
+                      int max_encoder_len, int* num_splits, size_t* need) {
+  kvq_status st = check_layer(ctx, layer);
+  if (st != KVQ_OK) return st;
+  if (!num_splits || *num_splits < 0 || batch < 0 || max_query_len < 0 || max_encoder_len < 0 ||
+      max_encoder_len > (1 << 30))
+    return KVQ_ERR_INVALID_ARG;
+  if (max_query_len == 0)                       // one query per sequence: the decode's plan
+    return kvq_decode_plan(ctx, layer, batch, max_encoder_len, num_splits, need);
+  const kvq_config& c = ctx->cfg;
+  const int tile = cross_query_tile(c.head_dim, c.num_q_heads / c.num_kv_heads);
+  const long long base = ((long long)max_query_len + tile - 1) / tile * batch * c.num_kv_heads;
+  const int tiles = (int)(((long long)max_encoder_len + CROSS_KEYS - 1) / CROSS_KEYS);
+  if (*num_splits == 0) *num_splits = plan_splits(base, tiles);
+  if (*num_splits > 1024 || base * *num_splits >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
+  *need = *num_splits <= 1 ? 0
+                           : (size_t)*num_splits * batch * (size_t)max_query_len * c.num_q_heads *
+                                 (c.head_dim + 1) * sizeof(float);
+  return KVQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -384,23 +407,18 @@ kvq_status kvq_copy_blocks(const kvq_ctx* ctx, int first_layer, int num_layers, 
 // ---------------------------------------------------------------- cross attention
 kvq_status kvq_cross_plan(const kvq_ctx* ctx, int layer, int batch, int max_query_len,
                           int max_encoder_len, int* num_splits, size_t* workspace_bytes) {
-  kvq_status st = check_layer(ctx, layer);
+  size_t need = 0;
+  kvq_status st =
+      plan_cross(ctx, layer, batch, max_query_len, max_encoder_len, num_splits, &need);
   if (st != KVQ_OK) return st;
-  if (!num_splits || *num_splits < 0 || batch < 0 || max_query_len < 0 || max_encoder_len < 0 ||
-      max_encoder_len > (1 << 30))
-    return KVQ_ERR_INVALID_ARG;
-  if (max_query_len == 0)                       // one query per sequence: the decode's plan
-    return kvq_decode_plan(ctx, layer, batch, max_encoder_len, num_splits, workspace_bytes);
-  const kvq_config& c = ctx->cfg;
-  const int tile = cross_query_tile(c.head_dim, c.num_q_heads / c.num_kv_heads);
-  const long long base = ((long long)max_query_len + tile - 1) / tile * batch * c.num_kv_heads;
-  const int tiles = (int)(((long long)max_encoder_len + CROSS_KEYS - 1) / CROSS_KEYS);
-  if (*num_splits == 0) *num_splits = plan_splits(base, tiles);
-  if (*num_splits > 1024 || base * *num_splits >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
-  if (workspace_bytes)
-    *workspace_bytes = *num_splits <= 1 ? 0
-                                        : (size_t)*num_splits * batch * (size_t)max_query_len *
-                                              c.num_q_heads * (c.head_dim + 1) * sizeof(float);
+  if (max_query_len == 1) {                     // the call may have no query_start: the decode's
+    int workers = 0;                            // own plan then fits the same workspace
+    size_t step = 0;
+    st = kvq_decode_plan(ctx, layer, batch, max_encoder_len, &workers, &step);
+    if (st != KVQ_OK) return st;
+    if (step > need) need = step;
+  }
+  if (workspace_bytes) *workspace_bytes = need;
   return KVQ_OK;
 }
 
@@ -416,14 +434,24 @@ kvq_status kvq_cross_attention(const kvq_ctx* ctx, int layer, const void* q, con
   if (ctx->window[layer] != 0) return KVQ_ERR_UNSUPPORTED;
   if (batch < 0 || max_query_len < 0 || max_encoder_len < 0 || max_blocks_per_seq < 0 || num_splits < 0)
     return KVQ_ERR_INVALID_ARG;
-  if (!query_start)
-    return max_query_len > 1
-               ? KVQ_ERR_INVALID_ARG
-               : kvq_decode_attention_bf16(ctx, layer, q, k_cache, v_cache, k_scale, v_scale,
-                                           k_cache_scale, v_cache_scale, block_table,
-                                           max_blocks_per_seq, encoder_lens, batch,
-                                           max_encoder_len, out, num_splits, workspace,
-                                           workspace_bytes, stream);
+  if (!query_start) {
+    if (max_query_len > 1) return KVQ_ERR_INVALID_ARG;
+    int workers = num_splits;
+    if (max_query_len == 1) {
+      // num_splits may count splits of the keys (kvq_cross_plan of 1), of which a
+      // single one would leave the batch to one warp: the decode's own plan, where
+      // the workspace holds it
+      int own = 0;
+      size_t step = 0;
+      st = kvq_decode_plan(ctx, layer, batch, max_encoder_len, &own, &step);
+      if (st != KVQ_OK) return st;
+      if (workspace_bytes >= step) workers = 0;
+    }
+    return kvq_decode_attention_bf16(ctx, layer, q, k_cache, v_cache, k_scale, v_scale,
+                                     k_cache_scale, v_cache_scale, block_table, max_blocks_per_seq,
+                                     encoder_lens, batch, max_encoder_len, out, workers, workspace,
+                                     workspace_bytes, stream);
+  }
   if (batch == 0 || max_query_len == 0) return KVQ_OK;
   const kvq_config& c = ctx->cfg;
   const int mode = ctx->mode[layer];
@@ -443,7 +471,7 @@ kvq_status kvq_cross_attention(const kvq_ctx* ctx, int layer, const void* q, con
   }
   int splits = num_splits;
   size_t need = 0;
-  st = kvq_cross_plan(ctx, layer, batch, max_query_len, max_encoder_len, &splits, &need);
+  st = plan_cross(ctx, layer, batch, max_query_len, max_encoder_len, &splits, &need);
   if (st != KVQ_OK) return st;
   if (splits > 1 && (!workspace || workspace_bytes < need)) return KVQ_ERR_WORKSPACE;
   if (splits > 1 && !aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
