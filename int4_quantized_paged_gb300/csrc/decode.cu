@@ -1196,40 +1196,6 @@ cudaError_t launch1(int D, int G, const DecodeArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeFn encode_fn() {
-  static EncodeFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                         cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeFn>(p);
-  }
-  return fn;
-}
-
-// The layer's code buffer as a 2-D uint8 tensor of 128-byte rows; one box is
-// a 16-position tile of one (block, KV head) page.
-bool make_tile_map(CUtensorMap* m, const void* base, long long total_bytes, int tile_bytes) {
-  EncodeFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {128, (cuuint64_t)(total_bytes / 128)};
-  cuuint64_t strides[1] = {128};
-  cuuint32_t box[2] = {128, (cuuint32_t)(tile_bytes / 128)};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int decode_ctas_per_sm(int mode, int D, int G) {
   switch (mode) {
     case BF16: return per_sm1<BF16>(D, G);

@@ -64,45 +64,6 @@
 namespace kvq {
 namespace {
 
-using WsEncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-WsEncodeFn ws_encode_fn() {
-  static WsEncodeFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<WsEncodeFn>(p);
-  }
-  return fn;
-}
-
-}  // namespace
-
-// A BF16 layer's K buffer as a 3-D uint8 tensor [cell][64-d block][128 bytes]:
-// one box is one 64-d block of 16 consecutive cells, which lands as 16 rows
-// of the K operand (128-byte swizzle).
-bool make_kblock_map(CUtensorMap* m, const void* base, long long total_bytes, int row_bytes) {
-  WsEncodeFn fn = ws_encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {128, (cuuint64_t)(row_bytes / 128), (cuuint64_t)(total_bytes / row_bytes)};
-  cuuint64_t strides[2] = {128, (cuuint64_t)row_bytes};
-  cuuint32_t box[3] = {128, 1, 16};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-namespace {
-
 template <int MODE, int D, int G>
 cudaError_t wslaunch3(const PrefillArgs& pa0, int max_query_len, cudaStream_t st) {
   using C = WCfg<MODE, D, false>;
