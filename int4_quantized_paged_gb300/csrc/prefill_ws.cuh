@@ -91,6 +91,7 @@ struct WRoles {
   static constexpr int REGS = 128;                   // a thread at launch (SPLIT_REGS)
   static constexpr int REGS_SOFT = 168, REGS_CONV = 112, REGS_REST = 64;
   static_assert(!SPLIT_REGS || 2 * REGS_SOFT + REGS_CONV + REGS_REST == 4 * REGS, "register shares");
+  static_assert(!SPLIT_REGS || (SOFT == 8 && PROD == 12 && THREADS == 16 * 32), "whole warpgroups");
 };
 constexpr int WKT = 64;                             // keys per tile
 constexpr int WKP = 6;                              // P' = p v_scale 2^(WKP - vexp) < 2^15 (p <= 2^8)
@@ -463,101 +464,205 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
   }
 
   // ================================================================ roles
-  if (warp == RL::PROD) {
-    // ---- producer: key tile t into raw stage (t - t0) % NR, page tile by page
-    // tile.  Page tiles wholly outside [kmin, pmax] are not fetched.  The block
-    // ids of 32 page tiles are loaded at once, one per lane and a round ahead, and
-    // every copy is issued by an elected lane from warp-uniform operands (copies
-    // issued by the page tiles' own lanes took a loop over the lanes each).
+  // A warpgroup's registers move where its branch begins, so that its four warps run
+  // one and the same setmaxnreg (it is undefined where they differ); warp 15 of
+  // SPLIT_REGS only completes the last one.
+  if (warp >= RL::PROD) {
     if constexpr (RL::SPLIT_REGS) give_registers<RL::REGS_REST>();
-    int last[NR];                                  // tile index last issued into each stage
+    if (warp == RL::PROD) {
+      // ---- producer: key tile t into raw stage (t - t0) % NR, page tile by page
+      // tile.  Page tiles wholly outside [kmin, pmax] are not fetched.  The block
+      // ids of 32 page tiles are loaded at once, one per lane and a round ahead, and
+      // every copy is issued by an elected lane from warp-uniform operands (copies
+      // issued by the page tiles' own lanes took a loop over the lanes each).
+      int last[NR];                                  // tile index last issued into each stage
 #pragma unroll
-    for (int s = 0; s < NR; ++s) last[s] = -1;
-    // block of page tile 32 c + lane (counted from the first key tile): -1 where
-    // nothing is to be fetched
-    auto block_ids = [&](int c) -> int {
-      const int pt = 32 * c + lane;
-      const int pos = t0 * WKT + 16 * pt;
-      if (pt >= SUB * ntl || pos + 16 <= kmin || pos > pmax) return -1;
-      const int blk = __ldg(a.block_table + (long long)b * a.max_blocks + (pos >> a.bs_shift));
-      if (blk >= 0 && blk < a.num_blocks) return blk;
-      atomicOr(a.err, ERR_BAD_INDEX);
-      return -1;
-    };
-    int ids = block_ids(0), ids_next = block_ids(1);
-    unsigned live = __ballot_sync(0xffffffffu, ids >= 0);
-    for (int i = 0; i < ntl; ++i) {
-      const int st = i % NR;
-      if (i >= NR) {
-        const bool ok = mbar_wait(&raw_empty[st], (uint32_t)((i / NR - 1) & 1));
-        if (!__all_sync(0xffffffffu, ok)) {
-          if (lane == 0) { *s_abort = 1; atomicOr(a.err, ERR_TIMEOUT); }
-          break;
-        }
-      }
-      if constexpr (C::KDIRECT) {
-        // K lands in operand buffer i % NB: wait until the MMAs of its last
-        // tile are done with it
-        if (i >= NB) {
-          const bool ok = mbar_wait(&kv_empty[i % NB], (uint32_t)((i / NB - 1) & 1));
+      for (int s = 0; s < NR; ++s) last[s] = -1;
+      // block of page tile 32 c + lane (counted from the first key tile): -1 where
+      // nothing is to be fetched
+      auto block_ids = [&](int c) -> int {
+        const int pt = 32 * c + lane;
+        const int pos = t0 * WKT + 16 * pt;
+        if (pt >= SUB * ntl || pos + 16 <= kmin || pos > pmax) return -1;
+        const int blk = __ldg(a.block_table + (long long)b * a.max_blocks + (pos >> a.bs_shift));
+        if (blk >= 0 && blk < a.num_blocks) return blk;
+        atomicOr(a.err, ERR_BAD_INDEX);
+        return -1;
+      };
+      int ids = block_ids(0), ids_next = block_ids(1);
+      unsigned live = __ballot_sync(0xffffffffu, ids >= 0);
+      for (int i = 0; i < ntl; ++i) {
+        const int st = i % NR;
+        if (i >= NR) {
+          const bool ok = mbar_wait(&raw_empty[st], (uint32_t)((i / NR - 1) & 1));
           if (!__all_sync(0xffffffffu, ok)) {
             if (lane == 0) { *s_abort = 1; atomicOr(a.err, ERR_TIMEOUT); }
             break;
           }
         }
-      }
-      if (__any_sync(0xffffffffu, *s_abort)) break;
-      const int at = (SUB * i) & 31;               // the tile's page tiles among the 32
-      if (at == 0 && i > 0) {
-        ids = ids_next;
-        live = __ballot_sync(0xffffffffu, ids >= 0);
-        ids_next = block_ids(SUB * i / 32 + 1);
-      }
-      const unsigned fetch = (live >> at) & ((1u << SUB) - 1u);
-      uint8_t* base = raw + st * C::RAWS;
-      fence_proxy_async();
-      if (elect_one()) {
-        s_have[st] = (int)fetch;
-        mbar_expect_tx(&raw_full[st], (uint32_t)__popc(fetch) * (2 * C::TB + (C::FETCH ? 128 : 0)));
-      }
-      __syncwarp();
-#pragma unroll
-      for (int s = 0; s < SUB; ++s) {
-        const unsigned blk = (unsigned)__shfl_sync(0xffffffffu, ids, at + s);
-        if (((fetch >> s) & 1u) && elect_one()) {
-          const int pos = (t0 + i) * WKT + 16 * s;
-          const unsigned cell = (blk * (unsigned)a.Hkv + (unsigned)g) * (unsigned)a.bs +
-                                (unsigned)(pos & (a.bs - 1));
-          const int rowc = (int)(((unsigned long long)cell * C::RB) >> 7);
-          if constexpr (C::KDIRECT) {
-            // bf16 K needs no conversion: each 64-d block of the page tile's 16
-            // rows goes to its rows of the K operand (K-major, 128-byte swizzle)
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-              tma_tile_3d(k16 + (i % NB) * C::KB + h * (WKT * 128) + s * (16 * 128), &kmap, 0, h,
-                          (int)cell, &raw_full[st]);
-          } else {
-            tma_tile_2d(base + s * C::TBP, &kmap, 0, rowc, &raw_full[st]);
-          }
-          tma_tile_2d(base + C::VOFF + s * C::TBP, &vmap, 0, rowc, &raw_full[st]);
-          if constexpr (C::FETCH) {
-            float* sc = reinterpret_cast<float*>(base + C::RAW);
-            bulk_copy(sc + 16 * s, a.k_cs + cell, 64, &raw_full[st]);
-            bulk_copy(sc + 16 * (SUB + s), a.v_cs + cell, 64, &raw_full[st]);
+        if constexpr (C::KDIRECT) {
+          // K lands in operand buffer i % NB: wait until the MMAs of its last
+          // tile are done with it
+          if (i >= NB) {
+            const bool ok = mbar_wait(&kv_empty[i % NB], (uint32_t)((i / NB - 1) & 1));
+            if (!__all_sync(0xffffffffu, ok)) {
+              if (lane == 0) { *s_abort = 1; atomicOr(a.err, ERR_TIMEOUT); }
+              break;
+            }
           }
         }
+        if (__any_sync(0xffffffffu, *s_abort)) break;
+        const int at = (SUB * i) & 31;               // the tile's page tiles among the 32
+        if (at == 0 && i > 0) {
+          ids = ids_next;
+          live = __ballot_sync(0xffffffffu, ids >= 0);
+          ids_next = block_ids(SUB * i / 32 + 1);
+        }
+        const unsigned fetch = (live >> at) & ((1u << SUB) - 1u);
+        uint8_t* base = raw + st * C::RAWS;
+        fence_proxy_async();
+        if (elect_one()) {
+          s_have[st] = (int)fetch;
+          mbar_expect_tx(&raw_full[st], (uint32_t)__popc(fetch) * (2 * C::TB + (C::FETCH ? 128 : 0)));
+        }
         __syncwarp();
-      }
-      last[st] = i;
-    }
-    // every copy issued has landed before the CTA exits (bounded waits)
-    if (lane == 0)
 #pragma unroll
-      for (int s = 0; s < NR; ++s)
-        if (last[s] >= 0) (void)mbar_wait(&raw_full[s], (uint32_t)((last[s] / NR) & 1));
-  } else if (warp >= RL::SOFT && warp < RL::PROD) {
-    // ---- converters (groups of 128 threads, taking key tiles in turn)
+        for (int s = 0; s < SUB; ++s) {
+          const unsigned blk = (unsigned)__shfl_sync(0xffffffffu, ids, at + s);
+          if (((fetch >> s) & 1u) && elect_one()) {
+            const int pos = (t0 + i) * WKT + 16 * s;
+            const unsigned cell = (blk * (unsigned)a.Hkv + (unsigned)g) * (unsigned)a.bs +
+                                  (unsigned)(pos & (a.bs - 1));
+            const int rowc = (int)(((unsigned long long)cell * C::RB) >> 7);
+            if constexpr (C::KDIRECT) {
+              // bf16 K needs no conversion: each 64-d block of the page tile's 16
+              // rows goes to its rows of the K operand (K-major, 128-byte swizzle)
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h)
+                tma_tile_3d(k16 + (i % NB) * C::KB + h * (WKT * 128) + s * (16 * 128), &kmap, 0, h,
+                            (int)cell, &raw_full[st]);
+            } else {
+              tma_tile_2d(base + s * C::TBP, &kmap, 0, rowc, &raw_full[st]);
+            }
+            tma_tile_2d(base + C::VOFF + s * C::TBP, &vmap, 0, rowc, &raw_full[st]);
+            if constexpr (C::FETCH) {
+              float* sc = reinterpret_cast<float*>(base + C::RAW);
+              bulk_copy(sc + 16 * s, a.k_cs + cell, 64, &raw_full[st]);
+              bulk_copy(sc + 16 * (SUB + s), a.v_cs + cell, 64, &raw_full[st]);
+            }
+          }
+          __syncwarp();
+        }
+        last[st] = i;
+      }
+      // every copy issued has landed before the CTA exits (bounded waits)
+      if (lane == 0)
+#pragma unroll
+        for (int s = 0; s < NR; ++s)
+          if (last[s] >= 0) (void)mbar_wait(&raw_full[s], (uint32_t)((last[s] / NR) & 1));
+    } else if (warp <= RL::MMA_PV) {
+      // ---- MMA issuers: one elected lane issues and commits (elect.sync picks the
+      // same lane each time: the warp is converged); the warp waits together.  S and
+      // PV have a warp each: one warp for both that waited for the P' of a query
+      // tile held up the other tile's next scores, and its waits and issues alone
+      // took 1,900 cycles of a key tile's 2,700.  With one query tile (FEW) there is
+      // nothing to hold up, and a second polling warp costs more (134 -> 143 us).
+      constexpr uint32_t IDS = mma_idesc<C::BFK>(WROWS, WKT);   // bf16 Q and K for BF16 layers
+      constexpr uint32_t IDO = mma_idesc<false>(WROWS, D) | MMA_B_MN_MAJOR;
+      auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
+        const bool w = __all_sync(0xffffffffu, mbar_wait(bar, par));
+        if (!w && lane == 0) { *s_abort = 1; atomicOr(a.err, ERR_TIMEOUT); }
+        return w && !__any_sync(0xffffffffu, *s_abort);
+      };
+      // Descriptors of the operand buffers' starts; an operand at byte offset
+      // o is the start's descriptor plus o / 16 (the 14-bit address field
+      // cannot carry: shared memory ends below 2^18 bytes)
+      const uint64_t dq = sw128_desc(q16), dk = sw128_desc(k16), dv = sw128_mn_desc(vt16, WKT * 128);
+      // S_j = Q_j K^T from K buffer kbuf into S buffer sb of query tile j (Q
+      // from shared memory with two query tiles, from tensor memory with one)
+      auto issue_s = [&](int j, int kbuf, int sb) {
+        const uint64_t qa = dq + (uint64_t)(j * (C::QB >> 4));
+        const uint64_t kb = dk + (uint64_t)(kbuf * (C::KB >> 4));
+        const uint32_t td = tmem + C::scol(j, sb);
+        if (elect_one()) {
+          tc_fence_after();
+#pragma unroll
+          for (int s2 = 0; s2 < D / 16; ++s2) {
+            const uint64_t db = kb + (uint64_t)((((s2 >> 2) * (WKT * 128)) + (s2 & 3) * 32) >> 4);
+            if constexpr (NQ == 2)
+              umma(td, qa + (uint64_t)((((s2 >> 2) * (WROWS * 128)) + (s2 & 3) * 32) >> 4), db, IDS,
+                   s2 > 0);
+            else
+              umma_tmem_a(td, tmem + C::QCOL + 8 * s2, db, IDS, s2 > 0);
+          }
+          umma_commit(&s_full[2 * j + sb]);
+        }
+        __syncwarp();
+      };
+      // O_j += P'_j V, every term of the split, P' from S/P' buffer sb, V from
+      // buffer vbuf
+      auto issue_pv = [&](int j, int vbuf, int sb, bool acc) {
+        const uint64_t vb = dv + (uint64_t)(vbuf * (C::VTB >> 4));
+        const uint32_t td = tmem + C::ocol(j);
+        const uint32_t ta = tmem + C::scol(j, sb);
+        if (elect_one()) {
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < PTERMS; ++h)
+#pragma unroll
+            for (int kk = 0; kk < WKT / 16; ++kk)
+              umma_tmem_a(td, ta + 32 * h + 8 * kk, vb + (uint64_t)(kk * (16 * 128 >> 4)), IDO,
+                          acc || h > 0 || kk > 0);
+          umma_commit(&pv_done[2 * j + sb]);
+        }
+        __syncwarp();
+      };
+      // S of key tile i goes into S/P' buffer i & 1 of each query tile, two tiles
+      // ahead of the softmax that reads it: S_j(i) is issued once PV_j(i-2), the
+      // last reader of that buffer's P', has completed, so the softmax of a query
+      // tile finds its next scores ready when it finishes
+      auto scores = [&](int i) -> bool {
+        bool go = wait(&kv_full[i % NB], (uint32_t)((i / NB) & 1));
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+          if (!go || j >= nqt) break;
+          if (i >= 2) go = wait(&pv_done[2 * j + (i & 1)], (uint32_t)(((i >> 1) - 1) & 1));
+          if (go) issue_s(j, i % NB, i & 1);
+        }
+        return go;
+      };
+      auto values = [&](int i) -> bool {
+        bool go = true;
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+          if (!go || j >= nqt) break;
+          go = wait(&p_full[2 * j + (i & 1)], (uint32_t)((i >> 1) & 1));
+          if (go) issue_pv(j, i % NB, i & 1, i > 0);
+        }
+        // every PV of this key tile has read its operands (and every S of it ended
+        // before its softmax): buffer free
+        if (go && elect_one()) umma_commit(&kv_empty[i % NB]);
+        __syncwarp();
+        return go;
+      };
+      bool go = true;
+      if constexpr (FEW) {
+        for (int i = 0; go && i < 2 && i < ntl; ++i) go = scores(i);
+        for (int i = 0; go && i < ntl; ++i) go = values(i) && (i + 2 >= ntl || scores(i + 2));
+      } else if (warp == RL::MMA_S) {
+        for (int i = 0; go && i < ntl; ++i) go = scores(i);
+      } else {
+        for (int i = 0; go && i < ntl; ++i) go = values(i);
+      }
+      // everything that this warp issued completes before the epilogue and the exit
+      uint64_t* fin = warp == RL::MMA_PV ? o_fin : s_fin;
+      if (elect_one()) umma_commit(fin);
+      __syncwarp();
+      (void)mbar_wait(fin, 0u);
+    }
+  } else if (warp >= RL::SOFT) {
     if constexpr (RL::SPLIT_REGS) give_registers<RL::REGS_CONV>();
+    // ---- converters (groups of 128 threads, taking key tiles in turn)
     const int cgrp = RL::CG == 1 ? 0 : (warp - RL::SOFT) / WS_CONV;
     const int ct_ = tid - (RL::SOFT + cgrp * WS_CONV) * 32;
     const int conv_bar = CONV_BAR + cgrp;
@@ -707,109 +812,6 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
         mbar_arrive(&kv_full[buf]);
       }
     }
-  } else if (warp == RL::MMA_S || warp == RL::MMA_PV) {
-    // ---- MMA issuers: one elected lane issues and commits (elect.sync picks the
-    // same lane each time: the warp is converged); the warp waits together.  S and
-    // PV have a warp each: one warp for both that waited for the P' of a query
-    // tile held up the other tile's next scores, and its waits and issues alone
-    // took 1,900 cycles of a key tile's 2,700.  With one query tile (FEW) there is
-    // nothing to hold up, and a second polling warp costs more (134 -> 143 us).
-    if constexpr (RL::SPLIT_REGS) give_registers<RL::REGS_REST>();
-    constexpr uint32_t IDS = mma_idesc<C::BFK>(WROWS, WKT);   // bf16 Q and K for BF16 layers
-    constexpr uint32_t IDO = mma_idesc<false>(WROWS, D) | MMA_B_MN_MAJOR;
-    auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
-      const bool w = __all_sync(0xffffffffu, mbar_wait(bar, par));
-      if (!w && lane == 0) { *s_abort = 1; atomicOr(a.err, ERR_TIMEOUT); }
-      return w && !__any_sync(0xffffffffu, *s_abort);
-    };
-    // Descriptors of the operand buffers' starts; an operand at byte offset
-    // o is the start's descriptor plus o / 16 (the 14-bit address field
-    // cannot carry: shared memory ends below 2^18 bytes)
-    const uint64_t dq = sw128_desc(q16), dk = sw128_desc(k16), dv = sw128_mn_desc(vt16, WKT * 128);
-    // S_j = Q_j K^T from K buffer kbuf into S buffer sb of query tile j (Q
-    // from shared memory with two query tiles, from tensor memory with one)
-    auto issue_s = [&](int j, int kbuf, int sb) {
-      const uint64_t qa = dq + (uint64_t)(j * (C::QB >> 4));
-      const uint64_t kb = dk + (uint64_t)(kbuf * (C::KB >> 4));
-      const uint32_t td = tmem + C::scol(j, sb);
-      if (elect_one()) {
-        tc_fence_after();
-#pragma unroll
-        for (int s2 = 0; s2 < D / 16; ++s2) {
-          const uint64_t db = kb + (uint64_t)((((s2 >> 2) * (WKT * 128)) + (s2 & 3) * 32) >> 4);
-          if constexpr (NQ == 2)
-            umma(td, qa + (uint64_t)((((s2 >> 2) * (WROWS * 128)) + (s2 & 3) * 32) >> 4), db, IDS,
-                 s2 > 0);
-          else
-            umma_tmem_a(td, tmem + C::QCOL + 8 * s2, db, IDS, s2 > 0);
-        }
-        umma_commit(&s_full[2 * j + sb]);
-      }
-      __syncwarp();
-    };
-    // O_j += P'_j V, every term of the split, P' from S/P' buffer sb, V from
-    // buffer vbuf
-    auto issue_pv = [&](int j, int vbuf, int sb, bool acc) {
-      const uint64_t vb = dv + (uint64_t)(vbuf * (C::VTB >> 4));
-      const uint32_t td = tmem + C::ocol(j);
-      const uint32_t ta = tmem + C::scol(j, sb);
-      if (elect_one()) {
-        tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < PTERMS; ++h)
-#pragma unroll
-          for (int kk = 0; kk < WKT / 16; ++kk)
-            umma_tmem_a(td, ta + 32 * h + 8 * kk, vb + (uint64_t)(kk * (16 * 128 >> 4)), IDO,
-                        acc || h > 0 || kk > 0);
-        umma_commit(&pv_done[2 * j + sb]);
-      }
-      __syncwarp();
-    };
-    // S of key tile i goes into S/P' buffer i & 1 of each query tile, two tiles
-    // ahead of the softmax that reads it: S_j(i) is issued once PV_j(i-2), the
-    // last reader of that buffer's P', has completed, so the softmax of a query
-    // tile finds its next scores ready when it finishes
-    auto scores = [&](int i) -> bool {
-      bool go = wait(&kv_full[i % NB], (uint32_t)((i / NB) & 1));
-#pragma unroll
-      for (int j = 0; j < NQ; ++j) {
-        if (!go || j >= nqt) break;
-        if (i >= 2) go = wait(&pv_done[2 * j + (i & 1)], (uint32_t)(((i >> 1) - 1) & 1));
-        if (go) issue_s(j, i % NB, i & 1);
-      }
-      return go;
-    };
-    auto values = [&](int i) -> bool {
-      bool go = true;
-#pragma unroll
-      for (int j = 0; j < NQ; ++j) {
-        if (!go || j >= nqt) break;
-        go = wait(&p_full[2 * j + (i & 1)], (uint32_t)((i >> 1) & 1));
-        if (go) issue_pv(j, i % NB, i & 1, i > 0);
-      }
-      // every PV of this key tile has read its operands (and every S of it ended
-      // before its softmax): buffer free
-      if (go && elect_one()) umma_commit(&kv_empty[i % NB]);
-      __syncwarp();
-      return go;
-    };
-    bool go = true;
-    if constexpr (FEW) {
-      for (int i = 0; go && i < 2 && i < ntl; ++i) go = scores(i);
-      for (int i = 0; go && i < ntl; ++i) go = values(i) && (i + 2 >= ntl || scores(i + 2));
-    } else if (warp == RL::MMA_S) {
-      for (int i = 0; go && i < ntl; ++i) go = scores(i);
-    } else {
-      for (int i = 0; go && i < ntl; ++i) go = values(i);
-    }
-    // everything that this warp issued completes before the epilogue and the exit
-    uint64_t* fin = warp == RL::MMA_PV ? o_fin : s_fin;
-    if (elect_one()) umma_commit(fin);
-    __syncwarp();
-    (void)mbar_wait(fin, 0u);
-  } else if (warp > RL::MMA_PV) {
-    // ---- completes the last warpgroup
-    if constexpr (RL::SPLIT_REGS) give_registers<RL::REGS_REST>();
   } else if (warp < 4 * nqt) {
     // ---- softmax of query tile j: one thread per row (its tensor-memory lane)
     if constexpr (RL::SPLIT_REGS) take_registers<RL::REGS_SOFT>();
