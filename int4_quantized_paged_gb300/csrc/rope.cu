@@ -11,10 +11,13 @@
 // Angles.  p f_i reaches 10^5 radians and more, where a 32-bit product keeps no
 // fraction of a turn.  The frequency is therefore held as a 64-bit fixed-point
 // fraction of a turn per position, F_i = f_i / (2 pi) 2^64: the product p F_i
-// wraps modulo one turn by itself, exactly, for any 64-bit p, and its upper 32
-// bits are the angle to 2^-32 of a turn.  cos and sin are then taken of a value
-// in [-pi, pi) in fp32.  The table comes with the launch as a parameter (128
-// entries at most), so the handle owns no device memory.
+// wraps modulo one turn by itself, exactly, for any 64-bit p.  The nearest quarter
+// turn comes off in integers too, so only the rest, an eighth of a turn at most, is
+// rounded to fp32, relative to its own size: sines and cosines near zero keep their
+// bits.  (Of the whole turn, fp32 is off by up to 9e-8 radians.)  What is left is
+// F_i's own rounding, a double's: about p f_i 2^-53 radians.  The table comes with
+// the launch as a parameter (128 entries at most), so the handle owns no device
+// memory.
 //
 // What bounds it: HBM.  Per token the kernel reads 2 D bytes for each q, k and
 // v head and writes 2 D for each q head and the codes and scales of k and v;
@@ -66,6 +69,17 @@ __device__ __forceinline__ void rotate(float* x, const float* c, const float* s)
     x[i0] = fmaf(a, c[j], -b * s[j]);
     x[i1] = fmaf(a, s[j], b * c[j]);
   }
+}
+
+// Sine and cosine of u 2^-64 of a turn.
+__device__ __forceinline__ void turn_sincos(unsigned long long u, float* sn, float* cn) {
+  const unsigned quarter = (unsigned)((u + (1ull << 61)) >> 62);        // modulo 4
+  const long long rest = (long long)(u - ((unsigned long long)quarter << 62));
+  float s, c;
+  sincospif((float)rest * 0x1p-63f, &s, &c);
+  const float s1 = quarter & 1u ? c : s, c1 = quarter & 1u ? -s : c;
+  *sn = quarter & 2u ? -s1 : s1;
+  *cn = quarter & 2u ? -c1 : c1;
 }
 
 // Vectors a lane has in flight.  Measured, 32,768 tokens x 80 heads of 128: 2: 217 us,
@@ -131,9 +145,8 @@ __global__ void __launch_bounds__(RWARPS * 32)
     for (int i = 0; i < NP; ++i) {
       const int p = lane + 32 * i;
       if (p < pairs) {
-        const int turn = (int)(((unsigned long long)pos * ph[i]) >> 32);   // turns x 2^32
         float sn, cn;
-        sincospif((float)turn * 0x1p-31f, &sn, &cn);
+        turn_sincos((unsigned long long)pos * ph[i], &sn, &cn);
         cs[p] = make_float2(cn * tab.magnitude, sn * a.sin_magnitude);
       }
     }
