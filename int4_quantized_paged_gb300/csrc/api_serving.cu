@@ -98,10 +98,17 @@ kvq_status plan_cross(const kvq_ctx* ctx, int layer, int batch, int max_query_le
     return kvq_decode_plan(ctx, layer, batch, max_encoder_len, num_splits, need);
   const kvq_config& c = ctx->cfg;
   const int tile = cross_query_tile(c.head_dim, c.num_q_heads / c.num_kv_heads);
-  const long long base = ((long long)max_query_len + tile - 1) / tile * batch * c.num_kv_heads;
+  // CTAs of one split, in steps whose products fit 64 bits
+  long long base = ((long long)max_query_len + tile - 1) / tile * batch;
+  if (base >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
+  base *= c.num_kv_heads;
+  if (base >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
   const int tiles = (int)(((long long)max_encoder_len + CROSS_KEYS - 1) / CROSS_KEYS);
   if (*num_splits == 0) *num_splits = plan_splits(base, tiles);
   if (*num_splits > 1024 || base * *num_splits >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
+  // the grid of the kernel that joins the splits
+  if (*num_splits > 1 && (long long)*num_splits * batch * max_query_len * c.num_q_heads >= (1LL << 34))
+    return KVQ_ERR_INVALID_ARG;
   *need = *num_splits <= 1 ? 0
                            : (size_t)*num_splits * batch * (size_t)max_query_len * c.num_q_heads *
                                  (c.head_dim + 1) * sizeof(float);
@@ -476,7 +483,6 @@ kvq_status kvq_cross_attention(const kvq_ctx* ctx, int layer, const void* q, con
   if (splits > 1 && (!workspace || workspace_bytes < need)) return KVQ_ERR_WORKSPACE;
   if (splits > 1 && !aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
   const size_t rows = (size_t)splits * batch * (size_t)max_query_len * c.num_q_heads;
-  if (rows >= (1ull << 31) * 8) return KVQ_ERR_INVALID_ARG;      // the joining kernel's grid
   unsigned* err = error_word();
   if (!err) return KVQ_ERR_CUDA;
   DecodeArgs a = {};
