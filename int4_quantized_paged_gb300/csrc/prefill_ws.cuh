@@ -94,6 +94,7 @@ struct WRoles {
   static_assert(!SPLIT_REGS || (SOFT == 8 && PROD == 12 && THREADS == 16 * 32), "whole warpgroups");
 };
 constexpr int WKT = 64;                             // keys per tile
+constexpr float NO_KEY = -INFINITY;                 // K scale that masks a key (0 is a scale: its scores are 0)
 constexpr int WKP = 6;                              // P' = p v_scale 2^(WKP - vexp) < 2^15 (p <= 2^8)
 constexpr float WLAZY = 8.f;                        // the reference max moves when exceeded by this
 // static FP8 scales: P' = p x 2^6 (< 2^14)
@@ -684,7 +685,7 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
       // fetched or the position lies outside [kmin, pmax].  Each thread takes NIT
       // chunks of each; all loads first, then conversions.  (KDIRECT: the producer
       // copied K there; rows of keys not fetched or outside the range hold whatever
-      // was there, and the softmax masks their scores by their K scale 0.)
+      // was there, and the softmax masks their scores by their K scale NO_KEY.)
       // WHOLE: every key of the tile fetched and in range, without the test per key.
       auto convert = [&](auto whole_tile) {
         constexpr bool WHOLE = decltype(whole_tile)::value;
@@ -779,7 +780,7 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
       else
         convert(std::false_type{});
       {
-        // scales: threads 0..63 K, 64..127 V (scale 0: no key)
+        // scales: threads 0..63 K, 64..127 V (no key: NO_KEY and 0)
         float* ksm = reinterpret_cast<float*>(scb + buf * C::SCS);
         float* vsm = ksm + WKT;
         int* tinfo = reinterpret_cast<int*>(vsm + WKT);
@@ -788,7 +789,7 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
         const int sub = key >> 4;
         const int pos = t * WKT + key;
         const bool live = ((have >> sub) & 1u) && pos >= kmin && pos <= pmax;
-        float sc = live ? 1.f : 0.f;
+        float sc = live ? 1.f : (isv ? 0.f : NO_KEY);
         if constexpr (C::FETCH)
           if (live) sc = reinterpret_cast<const float*>(base + C::RAW)[16 * (isv ? SUB + sub : sub) + (key & 15)];
         if constexpr (C::BFK) {
@@ -894,7 +895,7 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
         }
       } else {
         // keys of this row: [loA, pA] relative to the tile; a key outside the
-        // CTA's range or on a page not fetched has scale 0
+        // CTA's range or on a page not fetched has the scale NO_KEY
         const int kt0 = t * WKT + 16 * ch0;
         const int klo = loA - kt0, khi = pA < 0 ? -1 : pA - kt0;
 #pragma unroll
@@ -905,7 +906,7 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int k = 4 * k4 + e;
-            const bool okk = k >= klo && k <= khi && ksv[e] != 0.f;
+            const bool okk = k >= klo && k <= khi && ksv[e] != NO_KEY;
             x[e] = okk ? __uint_as_float(k < 32 ? s0[k] : s1[k - 32]) * ksv[e] : -INFINITY;
             m4[e] = fmaxf(m4[e], x[e]);
           }
