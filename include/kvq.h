@@ -288,13 +288,19 @@ kvq_status kvq_rope_cache_write(const kvq_ctx* ctx, const kvq_rope* rope, int la
  * Entries from query_start[num_rows] to max_tokens are filled with position 0
  * and slot -1 (a padded batch).
  * A row whose last block is partly filled and held by another entry too gets a
- * block of its own for it: copies[i] = (shared block, new block), which
- * kvq_copy_blocks must copy before anything is written; else (-1, -1).
+ * block of its own for it: copies[i] = (shared block, new block), else (-1, -1).
+ * That goes by the holders before the call: where all of them grow in one call,
+ * each takes a block, and the shared one is free with its page still to be read.
+ * kvq_copy_blocks(copies) therefore comes before anything is written AND before
+ * the next call that changes the pool, which may hand out or rename these blocks.
  * A row gets all that it asks for or nothing.  When the rows up to and including
  * row i need more blocks than are free, row i is refused if it needs any
  * (KVQ_ERR_NO_BLOCKS on the device word); when they have more than max_tokens
  * tokens it is refused too (KVQ_ERR_BAD_INDEX).  A refused row keeps its length
- * and table.  num_rows <= 4096; max_tokens < 2^31 - 1. */
+ * and table, but its tokens are counted: query_start runs past max_tokens where
+ * the tokens do, and an attention call with it then reads and writes rows that q
+ * and out have only if they are made for the sum of new_tokens.
+ * num_rows <= 4096; max_tokens < 2^31 - 1. */
 kvq_status kvq_extend_sequences(const kvq_ctx* ctx, const int* rows, const int* new_tokens,
                                 int num_rows, int* ref_count, int* block_table, int table_rows,
                                 int max_blocks_per_seq, int* context_lens, long long max_tokens,
@@ -311,7 +317,8 @@ kvq_status kvq_fork_sequences(const kvq_ctx* ctx, const int* parents, const int*
 
 /* Cuts row rows[i] (distinct rows) to its first min(length, keep_lens[i])
  * positions, or to none with keep_lens NULL: blocks past them lose a holder (and
- * are free when it was the last), their table entries become -1. */
+ * are free when it was the last), their table entries become -1 (one that names
+ * no block of the pool, too). */
 kvq_status kvq_truncate_sequences(const kvq_ctx* ctx, const int* rows, const int* keep_lens,
                                   int num_rows, int* ref_count, int* block_table, int table_rows,
                                   int max_blocks_per_seq, int* context_lens, void* stream);
@@ -322,7 +329,8 @@ kvq_status kvq_truncate_sequences(const kvq_ctx* ctx, const int* rows, const int
  *   moves      int32 [num_blocks / 2][2]  (old, new) id of each block that moved
  *   num_moves  int32 [1]                  their number; later entries are not written
  * kvq_copy_blocks(moves, num_blocks / 2, num_moves) then moves the pages of
- * every layer, before they are read or written. */
+ * every layer, before they are read or written and before the next call that
+ * changes the pool.  Copies that kvq_extend_sequences asked for come first. */
 kvq_status kvq_compact_blocks(const kvq_ctx* ctx, int* ref_count, int* block_table,
                               int table_rows, int max_blocks_per_seq, int* context_lens,
                               int* moves, int* num_moves, void* stream);
