@@ -510,8 +510,11 @@ kvq_status kvq_prefill_attention(const kvq_ctx* ctx, int layer, const void* q,
  *   the worker warps that the plan of 0 chooses, and num_splits of them only where
  *   the workspace is smaller than theirs.  The workspace (16-byte aligned) needs no
  *   initialisation; overlapping calls need one each.
- * Softmax and sums are fp32; the weight that meets a value is rounded to f16
- * (an eighth of the output's own rounding).  A layer with a window is
+ * Softmax and sums are fp32.  What meets a V code is the softmax weight (relative
+ * to the row's largest) times the V scale, rounded to f16: off by 2^-11 of itself, an
+ * eighth of the output's own rounding, while it is above 2^-20 of the largest V
+ * scale that the sequence has for the KV head, and by 2^-31 of that scale below
+ * (a BF16 layer's scale: the power of two of a V row's largest value over 2^14).  A layer with a window is
  * KVQ_ERR_UNSUPPORTED.  A length that is negative or past the table row sets
  * KVQ_ERR_BAD_INDEX and leaves that sequence's rows as they were (with
  * query_start NULL: as kvq_decode_attention treats it); a block id outside the

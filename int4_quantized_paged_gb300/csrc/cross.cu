@@ -13,8 +13,10 @@
 //    ragged lengths spread over the SMs and none waits for the longest.
 //  * The output is bf16, and the weight P' that meets V is one f16 term (11
 //    bits: off by 2^-11 of its value at most) where the fp32 prefill splits it in
-//    two.  That is an eighth of the output's own rounding (2^-8), the errors of many
-//    weights average, and the PV product costs one MMA instead of two.
+//    two.  That is an eighth of the output's own rounding (2^-8) while P' is a normal
+//    f16 number, that is for p x V scale above 2^-20 of the largest V scale seen;
+//    below, P' is off by 2^-31 of that scale.  The errors of many weights average,
+//    and the PV product costs one MMA instead of two.
 //
 //  * At most 128 rows (head_dim 64 and 128) take the FEW form: one query tile with
 //    Q in tensor memory, two converter groups, and 64 rows or fewer standing in
