@@ -120,11 +120,18 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+# The current stream's handle alone: a torch Stream object costs more than a small
+# launch, and torch.cuda.current_device() as much as the rest of _stream. A torch
+# without these two gets the handle from the Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # the handle alone: a torch Stream object costs more than a small launch, and
-        # torch.cuda.current_device() as much as the rest of this
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        if _raw_stream is None or _device is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
