@@ -57,6 +57,17 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
 }
 
+// The same for values that are bf16 already: their upper halves, so that what passes
+// through keeps its bits (the conversion makes every NaN the same).  Keeping the raw
+// words instead took 8 registers more: 194 -> 218 us for the 32,768 tokens below.
+__device__ __forceinline__ uint4 join8(const float* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = __byte_perm(__float_as_uint(x[2 * j]), __float_as_uint(x[2 * j + 1]), 0x7632);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Rotates the lane's 16 elements: pair j is (x[j], x[8 + j]) in the half layout
 // and (x[2j], x[2j + 1]) in the interleaved one.
 template <int LAYOUT>
@@ -171,12 +182,13 @@ __global__ void __launch_bounds__(RWARPS * 32)
         float x[16];
         unpack8(x, r0[u]);
         unpack8(x + 8, r1[u]);
-        if (rot && vv < hk) rotate<LAYOUT>(x, c, s);
+        const bool turned = rot && vv < hk;
+        if (turned) rotate<LAYOUT>(x, c, s);
         if (vv < a.Hq) {
           uint4* dst = reinterpret_cast<uint4*>(a.q_out + (long long)t * a.q_out_stride +
                                                 (long long)vv * D);
-          dst[c0] = pack8(x);
-          dst[c1] = pack8(x + 8);
+          dst[c0] = turned ? pack8(x) : join8(x);
+          dst[c1] = turned ? pack8(x + 8) : join8(x + 8);
           continue;
         }
         const int is_v = vv >= hk;
@@ -185,8 +197,8 @@ __global__ void __launch_bounds__(RWARPS * 32)
         uint8_t* cache = is_v ? w.v_cache : w.k_cache;
         if constexpr (MODE == BF16) {
           uint4* dst = reinterpret_cast<uint4*>(cache + (size_t)cell * (2 * D));
-          dst[c0] = pack8(x);
-          dst[c1] = pack8(x + 8);
+          dst[c0] = turned ? pack8(x) : join8(x);
+          dst[c1] = turned ? pack8(x + 8) : join8(x + 8);
         } else {
           float sc;
           if constexpr (MODE == FP8_PER_TENSOR) {
