@@ -581,7 +581,7 @@ kvq_status kvq_e4m3_encode(const float* in, unsigned char* out, long long n, voi
 kvq_status kvq_get_device_error(void* stream);
 
 /* Check of the timeout path (no counterpart on the pages).  Every wait of the
- * decode, prefill and staged cache-write kernels on a shared-memory barrier
+ * decode, prefill, cross and staged cache-write kernels on a shared-memory barrier
  * is bounded (about 2 s); a wait that runs out sets the TIMEOUT bit of the
  * device error word and the kernel stops instead of hanging the GPU.  This
  * call enqueues one warp that waits in the same way on a barrier that expects

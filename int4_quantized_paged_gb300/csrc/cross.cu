@@ -22,13 +22,14 @@
 //    Q in tensor memory, two converter groups, and 64 rows or fewer standing in
 //    the tile two or four times, each copy with its share of a key tile's keys.
 //
-// What bounds it.  Many queries: 4 D flops per row and key on the tensor cores; 8 x
-// 900-1,024 queries x 3,000-4,096 states, 32 heads of 128, FP8: 398 us, 1,124
-// TFLOP/s (0.58 of the cuBLAS bf16 rate); a softmax thread's chain of dependent
+// What bounds it.  Many queries: 4 D flops per row and key on the tensor cores; six
+// sequences of 900-1,024 queries x 3,000-4,096 states, 32 heads of 128, FP8 (and one
+// without states, one without queries): 400 us, 870 TFLOP/s (0.45 of the cuBLAS bf16
+// rate); a softmax thread's chain of dependent
 // steps takes about 1,880 cycles a key tile, the MMAs of the two query tiles
 // about 1,300 (those of S read Q from shared memory again for every 64 keys).
-// Few queries: the pages' bytes; 8 x 1-5 queries x 20,000-32,768 states, 64 heads:
-// 136 us, 3.2 TB/s (0.48); a key tile's 16 KB pass an SM in 770 cycles at the copy
+// Few queries: the pages' bytes; six sequences of 1-5 queries x 20,000-32,768 states,
+// 64 heads, likewise: 133 us, 2.6 TB/s (0.39); a key tile's 16 KB pass an SM in 770 cycles at the copy
 // rate and take about 1,450, in which its roles issue about half of the
 // instructions that the SM could: conversion and softmax cost the same for 5
 // rows as for 64.

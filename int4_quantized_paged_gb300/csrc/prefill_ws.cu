@@ -13,9 +13,9 @@
 // and streams the keys of both in tiles of 64 positions.  At head_dim 256 a
 // CTA owns one query tile (its O takes 256 tensor-memory columns) and keeps
 // Q in tensor memory, the A operand of S; the roles below then have one
-// softmax warpgroup and the other warps move down by four.  Roles (15 warps and one
-// that completes the last warpgroup; the softmax warpgroups take registers that the
-// others give up):
+// softmax warpgroup and the other warps move down by four.  Roles (15 warps; with
+// a scale per key one more, which completes the last warpgroup, and the softmax
+// warpgroups take registers that the others give up):
 //  * warp 12, producer: 2-D TMA copies of the key tile's K and V page tiles
 //    (and 64-byte bulk copies of their dynamic scales) into a ring of raw
 //    stages, issued by an elected lane; the block ids of 32 page tiles are
@@ -23,8 +23,8 @@
 //  * warps 8-11, converters: raw codes -> f16, K and V alike as 64 rows (keys)
 //    of D in 64-d blocks of 128-byte rows with the 128-byte swizzle: the
 //    K-major operand of S and the MN-major operand of PV, so nothing is
-//    transposed; K and V scales (zero for a key outside the CTA's range or on a
-//    page that was not fetched) and the tile's largest V-scale exponent.  Three
+//    transposed; K and V scales (a masking one and zero for a key outside the
+//    CTA's range or on a page that was not fetched) and the tile's largest V-scale exponent.  Three
 //    operand buffers.  BF16 layers:
 //    K stays bf16 (S is a bf16 MMA; at head_dim 128 the producer copies it
 //    straight into its operand buffer), and the converters give each V row
