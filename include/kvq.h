@@ -537,6 +537,38 @@ kvq_status kvq_cross_attention(const kvq_ctx* ctx, int layer, const void* q, con
 kvq_status kvq_cross_plan(const kvq_ctx* ctx, int layer, int batch, int max_query_len,
                           int max_encoder_len, int* num_splits, size_t* workspace_bytes);
 
+/* ------------------------------------------------- long and shared prompts
+ * Attention over whole prompts, before anything of them is cached: bf16 q, k and
+ * v as the projection (and kvq_rope_apply) leaves them, packed sequences, causal
+ * within each; kvq_cache_write then stores k and v.
+ *   out[t][hq] = sum_j softmax_j(softmax_scale <q[t][hq], k[j][h]>) v[j][h]
+ * over the tokens j of t's sequence with j <= t and, for a layer with a window W,
+ * j > t - W; h = hq / (Hq/Hkv).  The pages have no counterpart: they attend to a
+ * cache only.  Of `layer` the window is taken; its mode is not.
+ *
+ * q: bf16 [num_tokens][Hq][D], token t starting at element t * q_token_stride
+ *   (0 => Hq*D); k, v: bf16 [num_tokens][Hkv][D] with kv_token_stride (0 => Hkv*D).
+ *   16-byte aligned, strides multiples of 8 below 2^39; they may be parts of one
+ *   fused buffer.
+ * seq_start: device int32 [batch + 1], non-decreasing: sequence b is the tokens
+ *   [seq_start[b], seq_start[b + 1]), none included.  It need not start at 0 nor end
+ *   at num_tokens: tokens of no sequence are not computed, their rows of out stay
+ *   as they are, and their q, k and v may hold anything.
+ * max_seq_len: an upper bound of the sequences' lengths (sizes the grid); tokens
+ *   past it set KVQ_ERR_BAD_INDEX on the device word and are not computed.
+ * num_tokens: tokens that q, k, v and out hold, below 2^31 - 256.  A sequence with a
+ *   negative start or length, or past num_tokens, sets KVQ_ERR_BAD_INDEX; its rows
+ *   stay as they are.
+ * out: bf16 [num_tokens][Hq][D], 16-byte aligned; it overlaps none of q, k and v.
+ * Scores, softmax statistics and sums are fp32; the weight that meets v, relative
+ * to the row's largest (to within 2^8), is rounded to bf16, as the output is.
+ * Values of a sequence that are not finite may reach any of its rows, and no row of
+ * another sequence.  No workspace. */
+kvq_status kvq_prompt_attention(const kvq_ctx* ctx, int layer, const void* q,
+                                long long q_token_stride, const void* k, const void* v,
+                                long long kv_token_stride, const int* seq_start, int batch,
+                                int max_seq_len, long long num_tokens, void* out, void* stream);
+
 /* Decode attention that allocates nothing and needs no workspace from the
  * caller.  The pages have no counterpart to this call; it exists for callers
  * that cannot provide device scratch: code running where no device allocator

@@ -115,6 +115,20 @@ struct CopyArgs {
   unsigned* err;
 };
 
+// Attention over whole prompts (bf16 q, k and v, not cached).
+struct PromptArgs {
+  const uint16_t* q;           // bf16 [T][Hq][D], k and v [T][Hkv][D], with token strides
+  const int* seq_start;        // [B + 1]
+  uint16_t* out;               // bf16 [T][Hq][D]
+  unsigned* err;
+  long long T;
+  int B, Hq, Hkv, g_shift;     // 2^g_shift query heads per KV head
+  int max_len;                 // the caller's bound of a sequence's length
+  int window;
+  int qtiles;                  // set by the launcher: CTAs per (sequence, KV head)
+  float qk_scale;              // softmax_scale * log2(e)
+};
+
 // Launchers (return cudaGetLastError() of the launch).
 cudaError_t launch_cache_write(int mode, int D, const WriteArgs& a, cudaStream_t st);
 cudaError_t launch_rope(int mode, int D, int layout, RopeArgs a, const RopeTable& tab,
@@ -160,6 +174,16 @@ constexpr int CROSS_KEYS = 64;         // keys per tile; splits are whole tiles
 int cross_query_tile(int D, int G);    // queries of one (sequence, KV head) a CTA takes
 cudaError_t launch_cross(int mode, int D, int G, const DecodeArgs& a, const int* query_start,
                          int max_query_len, int splits, int split_tiles, cudaStream_t st);
+
+// bf16 rows [tokens][heads][D], `stride` elements between tokens, as boxes of
+// box_tokens x box_heads rows of 64 elements, 128B swizzle; the coordinates are
+// (byte of the row, head, token).  Tokens behind the last one read as zeros.
+bool make_rows_map(CUtensorMap* m, const void* base, int D, int heads, long long tokens,
+                   long long stride, int box_heads, int box_tokens);
+
+int prompt_positions_per_cta(int D, int G);
+cudaError_t launch_prompt(int D, const PromptArgs& a, long long q_stride, const void* k, const void* v,
+                          long long kv_stride, cudaStream_t st);
 
 // Device error word of the current device.
 unsigned* error_word();

@@ -63,4 +63,12 @@ bool make_kblock_map(CUtensorMap* m, const void* base, long long total_bytes, in
   return encode(m, 3, base, dims, strides, box);
 }
 
+bool make_rows_map(CUtensorMap* m, const void* base, int D, int heads, long long tokens,
+                   long long stride, int box_heads, int box_tokens) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D * 2, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {128, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  return encode(m, 3, base, dims, strides, box);
+}
+
 }  // namespace kvq

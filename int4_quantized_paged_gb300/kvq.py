@@ -88,6 +88,7 @@ _SIGS = {
     "kvq_cross_attention": (i32, [P, i32, P, P, P, P, P, P, P, P, i32, P, P, i32, i32, i32, P, i32,
                                   P, sz, P]),
     "kvq_cross_plan": (i32, [P, i32, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(sz)]),
+    "kvq_prompt_attention": (i32, [P, i32, P, i64, P, P, i64, P, i32, i32, i64, P, P]),
     "kvq_e4m3_encode": (i32, [P, P, i64, P]),
     "kvq_get_device_error": (i32, [P]),
     "kvq_check_bounded_wait": (i32, [i64, P]),
@@ -476,6 +477,18 @@ def kvq_cross_attention(ctx: Context, layer: int, q, k_cache, v_cache, block_tab
         _ptr(k_cache_scale), _ptr(v_cache_scale), _ptr(block_table), mb, _ptr(query_start),
         _ptr(encoder_lens), B, max_query_len, max_encoder_len, _ptr(out), num_splits,
         _ptr(workspace), workspace_bytes, _stream(stream)), "kvq_cross_attention")
+
+
+def kvq_prompt_attention(ctx: Context, layer: int, q, k, v, seq_start, out, *, max_seq_len: int,
+                         q_token_stride: int = 0, kv_token_stride: int = 0,
+                         num_tokens: Optional[int] = None, batch: Optional[int] = None, stream=None):
+    """Causal attention within each packed sequence of bf16 q, k and v that are not cached; bf16
+    output; see include/kvq.h."""
+    T = out.shape[0] if num_tokens is None else num_tokens
+    B = seq_start.shape[0] - 1 if batch is None else batch
+    _check(_lib.kvq_prompt_attention(ctx.handle, layer, _ptr(q), q_token_stride, _ptr(k), _ptr(v),
+                                     kv_token_stride, _ptr(seq_start), B, max_seq_len, T, _ptr(out),
+                                     _stream(stream)), "kvq_prompt_attention")
 
 
 def kvq_e4m3_encode(x, out, n: Optional[int] = None, stream=None):
