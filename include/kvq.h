@@ -569,6 +569,49 @@ kvq_status kvq_prompt_attention(const kvq_ctx* ctx, int layer, const void* q,
                                 long long kv_token_stride, const int* seq_start, int batch,
                                 int max_seq_len, long long num_tokens, void* out, void* stream);
 
+/* Eviction: cuts row rows[i] of one layer to its keep_lens[i] most wanted cells,
+ * for each KV head apart.  Of the L = context_lens[row] cells (logical positions of
+ * the table row) of a KV head the first first_kept and the last last_kept stay, and
+ * of those between the keep_lens[i] - first_kept - last_kept with the largest
+ * weights[row][h][p]; of equal weights the lowest p, NaN counts as the least.
+ * Attention over the first keep_lens[i] cells is then attention over these cells:
+ *   - cells of the middle that stay and lie below keep - last_kept keep their place;
+ *   - those that lie behind it go to the places of the evicted ones below it, the
+ *     i-th of them to the i-th place;
+ *   - the last last_kept cells go, in order, to [keep - last_kept, keep).
+ * Codes, dynamic scales and weights move together; weights[row][h][keep .. L) become
+ * 0, and the codes and scales there stay what they were.  What a cell's position in
+ * the sequence was (its rotation, a token's next position) does not change by this.
+ *
+ * The call reads and writes one layer and changes no length and no table: after
+ * the call for every layer of the pool, kvq_truncate_sequences(rows, new_lens) sets
+ * the lengths and gives the blocks back.  A layer with a window is
+ * KVQ_ERR_UNSUPPORTED.
+ *
+ * rows, keep_lens: device int32 [num_rows]; a row at most once.
+ * new_lens: device int32 [num_rows], written: min(L, keep_lens[i]), or L for a row
+ *   that is refused (below), or 0 where rows[i] itself is (kvq_truncate_sequences
+ *   refuses it then, too).
+ * ref_count: as for the page calls, read only, or NULL where the caller keeps none.
+ *   With it, a row of which another entry holds a block is refused: evicting would
+ *   change cells of the other row.
+ * block_table, table_rows, max_blocks_per_seq, context_lens: as for the page calls,
+ *   read only.
+ * max_context: an upper bound of context_lens, at most 393,216
+ *   (KVQ_ERR_UNSUPPORTED above).
+ * weights: device fp32 [table_rows][Hkv][weights_stride], weights_stride >=
+ *   max_context: what kvq_decode_attention_weights accumulated.
+ * A row outside the table or named before, a length that is negative, past the
+ * row's entries or past max_context, keep_lens[i] < first_kept + last_kept, a block
+ * outside the pool and a shared one set KVQ_ERR_BAD_INDEX on the device word and
+ * leave the row as it is; the others proceed.  No workspace. */
+kvq_status kvq_evict_cells(const kvq_ctx* ctx, int layer, const int* rows, const int* keep_lens,
+                           int num_rows, int first_kept, int last_kept, const int* ref_count,
+                           const int* block_table, int table_rows, int max_blocks_per_seq,
+                           const int* context_lens, int max_context, float* weights,
+                           long long weights_stride, int* new_lens, void* k_cache, void* v_cache,
+                           float* k_cache_scale, float* v_cache_scale, void* stream);
+
 /* Decode attention that allocates nothing and needs no workspace from the
  * caller.  The pages have no counterpart to this call; it exists for callers
  * that cannot provide device scratch: code running where no device allocator

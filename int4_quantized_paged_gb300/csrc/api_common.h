@@ -8,6 +8,7 @@
 #include <vector>
 
 #include "kvq.h"
+#include "kvq_internal.h"
 
 struct kvq_ctx {
   kvq_config cfg;
@@ -40,5 +41,30 @@ inline kvq_status check_layer(const kvq_ctx* ctx, int layer) {
 }
 
 inline kvq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
+
+inline PageTables page_tables(const kvq_ctx* ctx, int* ref_count, int* block_table, int rows,
+                              int max_blocks, int* context_lens, unsigned* err) {
+  PageTables t;
+  t.ref = ref_count;
+  t.table = block_table;
+  t.lens = context_lens;
+  t.num_blocks = ctx->cfg.num_blocks;
+  t.rows = rows;
+  t.max_blocks = max_blocks;
+  t.bs = ctx->cfg.block_size;
+  t.bs_shift = __builtin_ctz((unsigned)ctx->cfg.block_size);
+  t.err = err;
+  return t;
+}
+
+inline kvq_status check_tables(const kvq_ctx* ctx, const int* ref_count, const int* block_table,
+                               int rows, int max_blocks, const int* context_lens) {
+  if (!ctx || rows < 0 || max_blocks < 0) return KVQ_ERR_INVALID_ARG;
+  if ((long long)max_blocks * ctx->cfg.block_size >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
+  if (!ref_count || !block_table || !context_lens) return KVQ_ERR_INVALID_ARG;
+  if (!aligned4(ref_count) || !aligned4(block_table) || !aligned4(context_lens))
+    return KVQ_ERR_ALIGNMENT;
+  return KVQ_OK;
+}
 
 }  // namespace kvq

@@ -38,31 +38,6 @@ unsigned long long turn_fraction(double f) {
   return turns >= 1.0 ? 0ull : (unsigned long long)ldexp(turns, 64);
 }
 
-PageTables page_tables(const kvq_ctx* ctx, int* ref_count, int* block_table, int rows, int max_blocks,
-                       int* context_lens, unsigned* err) {
-  PageTables t;
-  t.ref = ref_count;
-  t.table = block_table;
-  t.lens = context_lens;
-  t.num_blocks = ctx->cfg.num_blocks;
-  t.rows = rows;
-  t.max_blocks = max_blocks;
-  t.bs = ctx->cfg.block_size;
-  t.bs_shift = __builtin_ctz((unsigned)ctx->cfg.block_size);
-  t.err = err;
-  return t;
-}
-
-kvq_status check_tables(const kvq_ctx* ctx, const int* ref_count, const int* block_table, int rows,
-                        int max_blocks, const int* context_lens) {
-  if (!ctx || rows < 0 || max_blocks < 0) return KVQ_ERR_INVALID_ARG;
-  if ((long long)max_blocks * ctx->cfg.block_size >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
-  if (!ref_count || !block_table || !context_lens) return KVQ_ERR_INVALID_ARG;
-  if (!aligned4(ref_count) || !aligned4(block_table) || !aligned4(context_lens))
-    return KVQ_ERR_ALIGNMENT;
-  return KVQ_OK;
-}
-
 // Splits of the keys for `base` CTAs (query tiles x sequences x KV heads) over
 // `tiles` key tiles: the count whose waves over the SMs take the least time, in
 // units of a key tile (about 1 us): a CTA costs its tiles and about three more

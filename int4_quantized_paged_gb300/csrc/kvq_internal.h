@@ -129,6 +129,21 @@ struct PromptArgs {
   float qk_scale;              // softmax_scale * log2(e)
 };
 
+// Eviction of the cells with the least accumulated weight.
+struct EvictArgs {
+  PageTables t;
+  const int* rows;             // [n]
+  const int* keep_lens;        // [n]
+  int* new_lens;               // [n]
+  float* weights;              // [table rows][Hkv][stride]
+  long long stride;
+  uint8_t* code[2];            // K and V codes
+  float* scale[2];             // dynamic modes (else nullptr)
+  int Hkv, first, last, max_len;
+  int chunk_shift;             // log2 of a cell's 16-byte chunks in one code buffer
+  int seg_max;                 // set by the launcher: cells of a CTA at most
+};
+
 // Launchers (return cudaGetLastError() of the launch).
 cudaError_t launch_cache_write(int mode, int D, const WriteArgs& a, cudaStream_t st);
 cudaError_t launch_rope(int mode, int D, int layout, RopeArgs a, const RopeTable& tab,
@@ -184,6 +199,10 @@ bool make_rows_map(CUtensorMap* m, const void* base, int D, int heads, long long
 int prompt_positions_per_cta(int D, int G);
 cudaError_t launch_prompt(int D, const PromptArgs& a, long long q_stride, const void* k, const void* v,
                           long long kv_stride, cudaStream_t st);
+
+// CTAs per (row, KV head) of an eviction; 0: no cluster holds max_len weights.
+int evict_cluster(int max_len, long long items);
+cudaError_t launch_evict(EvictArgs a, int n, cudaStream_t st);
 
 // Device error word of the current device.
 unsigned* error_word();

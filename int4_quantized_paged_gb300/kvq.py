@@ -89,6 +89,8 @@ _SIGS = {
                                   P, sz, P]),
     "kvq_cross_plan": (i32, [P, i32, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(sz)]),
     "kvq_prompt_attention": (i32, [P, i32, P, i64, P, P, i64, P, i32, i32, i64, P, P]),
+    "kvq_evict_cells": (i32, [P, i32, P, P, i32, i32, i32, P, P, i32, i32, P, i32, P, i64, P, P, P, P,
+                              P, P]),
     "kvq_e4m3_encode": (i32, [P, P, i64, P]),
     "kvq_get_device_error": (i32, [P]),
     "kvq_check_bounded_wait": (i32, [i64, P]),
@@ -489,6 +491,20 @@ def kvq_prompt_attention(ctx: Context, layer: int, q, k, v, seq_start, out, *, m
     _check(_lib.kvq_prompt_attention(ctx.handle, layer, _ptr(q), q_token_stride, _ptr(k), _ptr(v),
                                      kv_token_stride, _ptr(seq_start), B, max_seq_len, T, _ptr(out),
                                      _stream(stream)), "kvq_prompt_attention")
+
+
+def kvq_evict_cells(ctx: Context, layer: int, rows, keep_lens, block_table, context_lens, weights, new_lens,
+                    k_cache, v_cache, k_cache_scale=None, v_cache_scale=None, *, first_kept: int,
+                    last_kept: int, max_context: int, ref_count=None, weights_stride: Optional[int] = None,
+                    stream=None):
+    """Cuts each row to keep_lens[i] cells per KV head, those of the most accumulated weight among
+    them; weights: fp32 [table rows, Hkv, stride]; see include/kvq.h."""
+    stride = weights.shape[2] if weights_stride is None else weights_stride
+    _check(_lib.kvq_evict_cells(
+        ctx.handle, layer, _ptr(rows), _ptr(keep_lens), rows.numel(), first_kept, last_kept, _ptr(ref_count),
+        _ptr(block_table), block_table.shape[0], block_table.shape[1], _ptr(context_lens), max_context,
+        _ptr(weights), stride, _ptr(new_lens), _ptr(k_cache), _ptr(v_cache), _ptr(k_cache_scale),
+        _ptr(v_cache_scale), _stream(stream)), "kvq_evict_cells")
 
 
 def kvq_e4m3_encode(x, out, n: Optional[int] = None, stream=None):
