@@ -569,6 +569,90 @@ kvq_status kvq_prompt_attention(const kvq_ctx* ctx, int layer, const void* q,
                                 long long kv_token_stride, const int* seq_start, int batch,
                                 int max_seq_len, long long num_tokens, void* out, void* stream);
 
+/* Decode attention of a batch whose rows share prefixes (a system prompt, a long
+ * document, the beams of a search): what kvq_decode_attention computes, one query
+ * token per row, with each group's prefix read once for all its rows instead of once
+ * for each.
+ *
+ * Group g is the rows [group_start[g], group_start[g + 1]), and the first
+ * shared_lens[g] positions of its rows hold the same keys and values: blocks that
+ * kvq_fork_sequences shares, or copies of them, as a row that grew has one of the
+ * last, partly filled block.  They are read through the table row of the group's
+ * first row.  A row attends to all of its context_lens[b] positions, those of the
+ * prefix among them; a prefix longer than a row of the group is cut to that row.
+ *
+ * q: bf16 [batch][Hq][D]; out: bf16 [batch][Hq][D], both 16-byte aligned.  L = 0
+ *   gives a zero row.
+ * block_table, max_blocks_per_seq, context_lens: as for kvq_decode_attention, whole
+ *   rows (a prefix need not be shared for the result to be right).
+ * group_start: device int32 [num_groups + 1], non-decreasing, within [0, batch]; rows
+ *   of no group read all of their positions.  shared_lens: device int32 [num_groups].
+ *   num_groups 0: both may be NULL.
+ * max_group: an upper bound of a group's rows; the rows of a larger group read the
+ *   prefix each for itself (so do groups of one row).
+ * max_shared, max_own: upper bounds of shared_lens and of a row's positions behind
+ *   its prefix, for the plan only.
+ * num_splits, workspace: from kvq_shared_prefix_plan with the same sizes; num_splits 0
+ *   = the plan's choice.  The workspace (16-byte aligned) needs no initialisation;
+ *   overlapping calls need one each.
+ * Softmax and sums are fp32; over the prefix, the weight that meets a V code is
+ * rounded as kvq_cross_attention says.  A layer with a window is
+ * KVQ_ERR_UNSUPPORTED (it reads no long prefix).  A group with a negative start or
+ * length, past the batch, or with a negative shared length sets KVQ_ERR_BAD_INDEX and
+ * shares nothing; lengths and block ids as kvq_decode_attention treats them.  Scale
+ * pointers as for kvq_decode_attention. */
+kvq_status kvq_shared_prefix_attention(const kvq_ctx* ctx, int layer, const void* q,
+                                       const void* k_cache, const void* v_cache,
+                                       const float* k_scale, const float* v_scale,
+                                       const float* k_cache_scale, const float* v_cache_scale,
+                                       const int* block_table, int max_blocks_per_seq,
+                                       const int* context_lens, int batch, const int* group_start,
+                                       const int* shared_lens, int num_groups, int max_group,
+                                       int max_shared, int max_own, void* out, int num_splits,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Splits of the prefixes and workspace bytes of a kvq_shared_prefix_attention call: on
+ * input *num_splits > 0 (at most 1024) requests a count, 0 asks for the plan's choice;
+ * on output it is 0 where nothing can be shared (no group of two rows, or no prefix of
+ * 16 positions). */
+kvq_status kvq_shared_prefix_plan(const kvq_ctx* ctx, int layer, int batch, int num_groups,
+                                  int max_group, int max_shared, int max_own, int* num_splits,
+                                  size_t* workspace_bytes);
+
+/* Decode attention that also accumulates how much weight each cell gets:
+ *   weights[b][h][p] = decay weights[b][h][p]
+ *                      + sum over the query heads of KV head h of softmax_p(...)
+ * for p < context_lens[b], with the softmax that kvq_decode_attention weights V by;
+ * later entries are not touched.  kvq_evict_cells chooses by these sums.
+ *
+ * Arguments, output and errors as for kvq_decode_attention_bf16, except:
+ * max_context: a bound that counts: a longer context is an index error, of which the
+ *   first max_context positions are read (and weighted).
+ * decay: in [0, 1]; 1 adds up, below 1 older steps fade.
+ * weights: device fp32 [batch][Hkv][weights_stride], weights_stride >= max_context,
+ *   row b being that of context_lens[b].  A cell that has been written since has to
+ *   start from 0: zero a row when its sequence begins (kvq_evict_cells does so for
+ *   the places that it frees).  Rows must not overlap.
+ * num_workers, workspace: from kvq_decode_weights_plan; the workspace (16-byte
+ *   aligned, no initialisation) holds the scores, so it is needed with one worker
+ *   too.  A layer with a window is KVQ_ERR_UNSUPPORTED.  batch <= 65535.
+ * The sums do not depend on the order of atomics: the same call gives the same bits.
+ * A weight is exact to a few times 2^-24 of itself and of the scores' size. */
+kvq_status kvq_decode_attention_weights(const kvq_ctx* ctx, int layer, const void* q,
+                                        const void* k_cache, const void* v_cache,
+                                        const float* k_scale, const float* v_scale,
+                                        const float* k_cache_scale, const float* v_cache_scale,
+                                        const int* block_table, int max_blocks_per_seq,
+                                        const int* context_lens, int batch, int max_context,
+                                        void* out, float decay, float* weights,
+                                        long long weights_stride, int num_workers,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Worker warps and workspace bytes of a kvq_decode_attention_weights call (num_workers
+ * as for kvq_decode_plan). */
+kvq_status kvq_decode_weights_plan(const kvq_ctx* ctx, int layer, int batch, int max_context,
+                                   int* num_workers, size_t* workspace_bytes);
+
 /* Eviction: cuts row rows[i] of one layer to its keep_lens[i] most wanted cells,
  * for each KV head apart.  Of the L = context_lens[row] cells (logical positions of
  * the table row) of a KV head the first first_kept and the last last_kept stay, and

@@ -17,7 +17,7 @@ OUT = os.path.join(PKG, "libkvq.so")
 BUILD = os.path.join(PKG, "_build")
 SOURCES = ["api.cu", "api_serving.cu", "tensor_map.cu", "write.cu", "rope.cu", "pages.cu", "decode.cu",
            "prefill.cu", "prefill_ws.cu", "cross.cu", "api_prompts.cu", "prompt.cu",
-           "evict.cu"]
+           "shared.cu", "decode_weights.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

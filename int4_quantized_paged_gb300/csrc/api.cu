@@ -278,7 +278,7 @@ kvq_status decode_impl(const kvq_ctx* ctx, int layer, const void* q, const float
   unsigned* err = kvq::error_word();
   if (!err) return KVQ_ERR_CUDA;
   const int G = c.num_q_heads / c.num_kv_heads;
-  kvq::DecodeArgs a;
+  kvq::DecodeArgs a = {};
   a.q = static_cast<const uint16_t*>(q);
   a.q_scale = q_scale;
   a.q_scale_count = q_scale ? q_scale_count : 0;
@@ -305,6 +305,7 @@ kvq_status decode_impl(const kvq_ctx* ctx, int layer, const void* q, const float
   a.bs = c.block_size;
   a.bs_shift = __builtin_ctz((unsigned)c.block_size);
   a.max_blocks = max_blocks_per_seq;
+  a.cap = (long long)max_blocks_per_seq * c.block_size;
   a.window = ctx->window[layer];
   a.workers = workers;
   a.num_blocks = c.num_blocks;

@@ -67,4 +67,7 @@ inline kvq_status check_tables(const kvq_ctx* ctx, const int* ref_count, const i
   return KVQ_OK;
 }
 
+// Splits of the keys of an attention without a mask (api_serving.cu).
+int plan_splits(long long base, int tiles);
+
 }  // namespace kvq

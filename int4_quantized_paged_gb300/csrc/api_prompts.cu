@@ -9,6 +9,130 @@
 
 using namespace kvq;
 
+namespace {
+
+size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+// Bytes of the decode kernel's partials and of the items' offsets in its tile list.
+size_t partial_bytes(const kvq_config& c, int batch, int workers) {
+  const size_t items = (size_t)batch * c.num_kv_heads, slots = items + (size_t)workers;
+  const size_t G = c.num_q_heads / c.num_kv_heads;
+  return align16(slots * G * (c.head_dim + 2) * sizeof(float) + (items + 1) * sizeof(long long));
+}
+
+// The partials' places in a workspace of partial_bytes.
+void place_partials(const kvq_config& c, DecodeArgs* a, uint8_t* at) {
+  const size_t slots = (size_t)a->B * c.num_kv_heads + (size_t)a->workers;
+  const size_t rows = slots * (c.num_q_heads / c.num_kv_heads);
+  a->ws_o = reinterpret_cast<float*>(at);
+  a->ws_ml = a->ws_o + rows * c.head_dim;
+  a->item_tiles = reinterpret_cast<long long*>(a->ws_ml + rows * 2);
+}
+
+// The arguments that the decode calls of this file have in common: checked, and put
+// into *a.
+kvq_status decode_args(const kvq_ctx* ctx, int layer, const void* q, const void* k_cache,
+                       const void* v_cache, const float* k_scale, const float* v_scale,
+                       const float* k_cache_scale, const float* v_cache_scale,
+                       const int* block_table, int max_blocks_per_seq, const int* context_lens,
+                       int batch, int max_context, void* out, DecodeArgs* a) {
+  const kvq_config& c = ctx->cfg;
+  const int mode = ctx->mode[layer];
+  if ((long long)max_context > (long long)max_blocks_per_seq * c.block_size)
+    return KVQ_ERR_INVALID_ARG;
+  if (!q || !k_cache || !v_cache || !block_table || !context_lens || !out)
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      !aligned4(block_table) || !aligned4(context_lens))
+    return KVQ_ERR_ALIGNMENT;
+  if ((mode == KVQ_FP8_PER_TENSOR || mode == KVQ_FP8_PER_HEAD) && (!k_scale || !v_scale))
+    return KVQ_ERR_INVALID_ARG;
+  if (is_dynamic(mode)) {
+    if (!k_cache_scale || !v_cache_scale) return KVQ_ERR_INVALID_ARG;
+    // the kernels fetch 16 scales at a time by bulk copies
+    if (!aligned16(k_cache_scale) || !aligned16(v_cache_scale)) return KVQ_ERR_ALIGNMENT;
+  }
+  *a = {};
+  a->q = static_cast<const uint16_t*>(q);
+  a->k_cache = static_cast<const uint8_t*>(k_cache);
+  a->v_cache = static_cast<const uint8_t*>(v_cache);
+  a->k_scale = k_scale;
+  a->v_scale = v_scale;
+  a->k_cs = k_cache_scale;
+  a->v_cs = v_cache_scale;
+  a->block_table = block_table;
+  a->context_lens = context_lens;
+  a->out_bf16 = static_cast<uint16_t*>(out);
+  a->B = batch;
+  a->Hq = c.num_q_heads;
+  a->Hkv = c.num_kv_heads;
+  a->bs = c.block_size;
+  a->bs_shift = __builtin_ctz((unsigned)c.block_size);
+  a->max_blocks = max_blocks_per_seq;
+  a->cap = (long long)max_blocks_per_seq * c.block_size;
+  a->num_blocks = c.num_blocks;
+  a->qk_scale = ctx->softmax_scale * 1.4426950408889634f;
+  return KVQ_OK;
+}
+
+// Pages that cannot stay in L2 until the next step are streamed evict-first.
+int stream_once(const kvq_ctx* ctx, int layer, int batch, long long positions) {
+  const kvq_config& c = ctx->cfg;
+  const int mode = ctx->mode[layer];
+  const double bytes = (double)batch * c.num_kv_heads * (double)positions *
+                       (2.0 * (double)row_bytes(mode, c.head_dim) + (is_dynamic(mode) ? 8 : 0));
+  return bytes > 64.0 * 1024 * 1024;
+}
+
+constexpr long long kMostWorkers = 4LL * 65535 * 64;
+
+// Sizes of a call behind shared prefixes: splits (0 in: the plan's choice), workers of
+// the rows' own positions, and the parts of the workspace.
+struct SharedPlan {
+  int splits, workers;
+  size_t rows;                   // partial rows of the prefixes
+  size_t index_bytes, prefix_bytes, own_bytes;
+  size_t bytes() const { return index_bytes + prefix_bytes + own_bytes; }
+};
+
+kvq_status plan_shared(const kvq_ctx* ctx, int layer, int batch, int num_groups, int max_group,
+                       int max_shared, int max_own, int num_splits, SharedPlan* p) {
+  kvq_status st = check_layer(ctx, layer);
+  if (st != KVQ_OK) return st;
+  if (ctx->window[layer] != 0) return KVQ_ERR_UNSUPPORTED;
+  if (batch < 0 || num_groups < 0 || max_group < 0 || max_shared < 0 || max_own < 0 ||
+      max_shared > (1 << 30) || max_own > (1 << 30) || num_splits < 0 || num_splits > 1024)
+    return KVQ_ERR_INVALID_ARG;
+  const kvq_config& c = ctx->cfg;
+  if (max_group > batch) max_group = batch;
+  *p = {};
+  if (num_groups > 0 && max_group > 1 && max_shared >= 16) {
+    const int tile = cross_query_tile(c.head_dim, c.num_q_heads / c.num_kv_heads);
+    // CTAs of one split, in steps whose products fit 64 bits
+    long long base = ((long long)max_group + tile - 1) / tile * num_groups;
+    if (base >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
+    base *= c.num_kv_heads;
+    if (base >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
+    const int tiles = (int)(((long long)max_shared + CROSS_KEYS - 1) / CROSS_KEYS);
+    p->splits = num_splits > 0 ? num_splits : plan_splits(base, tiles);
+    if (base * p->splits >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
+    const long long rows = (long long)num_groups * max_group;      // below 2^62
+    if (rows >= (1LL << 34) / p->splits / c.num_q_heads) return KVQ_ERR_INVALID_ARG;
+    p->rows = (size_t)p->splits * (size_t)rows * c.num_q_heads;
+  }
+  // a prefix is cut to whole tiles of 16, and what is left over is a row's own
+  int workers = 0;
+  st = kvq_decode_plan(ctx, layer, batch, max_own + 15, &workers, nullptr);
+  if (st != KVQ_OK) return st;
+  p->workers = workers;
+  p->index_bytes = align16(((size_t)batch * 2 + (size_t)num_groups) * sizeof(int));
+  p->prefix_bytes = align16(p->rows * (c.head_dim + 1) * sizeof(float));
+  p->own_bytes = partial_bytes(c, batch, workers);
+  return KVQ_OK;
+}
+
+}  // namespace
+
 extern "C" {
 
 kvq_status kvq_prompt_attention(const kvq_ctx* ctx, int layer, const void* q,
@@ -53,6 +177,131 @@ kvq_status kvq_prompt_attention(const kvq_ctx* ctx, int layer, const void* q,
   a.qk_scale = ctx->softmax_scale * 1.4426950408889634f;
   return cuda_status(
       launch_prompt(c.head_dim, a, qs, k, v, ks, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- shared prefixes
+kvq_status kvq_shared_prefix_plan(const kvq_ctx* ctx, int layer, int batch, int num_groups,
+                                  int max_group, int max_shared, int max_own, int* num_splits,
+                                  size_t* workspace_bytes) {
+  if (!num_splits) return KVQ_ERR_INVALID_ARG;
+  SharedPlan p;
+  const kvq_status st = plan_shared(ctx, layer, batch, num_groups, max_group, max_shared, max_own,
+                                    *num_splits, &p);
+  if (st != KVQ_OK) return st;
+  *num_splits = p.splits;
+  if (workspace_bytes) *workspace_bytes = p.bytes();
+  return KVQ_OK;
+}
+
+kvq_status kvq_shared_prefix_attention(const kvq_ctx* ctx, int layer, const void* q,
+                                       const void* k_cache, const void* v_cache,
+                                       const float* k_scale, const float* v_scale,
+                                       const float* k_cache_scale, const float* v_cache_scale,
+                                       const int* block_table, int max_blocks_per_seq,
+                                       const int* context_lens, int batch, const int* group_start,
+                                       const int* shared_lens, int num_groups, int max_group,
+                                       int max_shared, int max_own, void* out, int num_splits,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  SharedPlan p;
+  kvq_status st = plan_shared(ctx, layer, batch, num_groups, max_group, max_shared, max_own,
+                              num_splits, &p);
+  if (st != KVQ_OK) return st;
+  if (max_blocks_per_seq < 0) return KVQ_ERR_INVALID_ARG;
+  if (batch == 0) return KVQ_OK;
+  const kvq_config& c = ctx->cfg;
+  DecodeArgs a;
+  st = decode_args(ctx, layer, q, k_cache, v_cache, k_scale, v_scale, k_cache_scale, v_cache_scale,
+                   block_table, max_blocks_per_seq, context_lens, batch, 0, out, &a);
+  if (st != KVQ_OK) return st;
+  if ((long long)max_blocks_per_seq * c.block_size >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
+  if (num_groups > 0 && (!group_start || !shared_lens)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned4(group_start) || !aligned4(shared_lens)) return KVQ_ERR_ALIGNMENT;
+  if ((long long)batch * c.num_q_heads >= (1LL << 31) || p.workers > kMostWorkers)
+    return KVQ_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < p.bytes()) return KVQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
+  a.err = error_word();
+  if (!a.err) return KVQ_ERR_CUDA;
+  a.workers = p.workers;
+  a.stream_once = stream_once(ctx, layer, batch, max_own);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  SharedArgs x = {};
+  x.group_start = group_start;
+  x.shared_lens = shared_lens;
+  x.groups = num_groups;
+  x.max_group = max_group < batch ? max_group : batch;
+  x.splits = p.splits;
+  const int tiles = (max_shared + CROSS_KEYS - 1) / CROSS_KEYS;
+  x.split_tiles = p.splits > 0 ? (tiles + p.splits - 1) / p.splits : 1;
+  x.first = reinterpret_cast<int*>(ws);
+  x.group_of = x.first + batch;
+  x.prefix = x.group_of + batch;
+  x.o = reinterpret_cast<float*>(ws + p.index_bytes);
+  x.lse = x.o + p.rows * c.head_dim;
+  a.first = x.first;
+  place_partials(c, &a, ws + p.index_bytes + p.prefix_bytes);
+  return cuda_status(launch_shared(ctx->mode[layer], c.head_dim, c.num_q_heads / c.num_kv_heads, a,
+                                   x, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- accumulated weights
+kvq_status kvq_decode_weights_plan(const kvq_ctx* ctx, int layer, int batch, int max_context,
+                                   int* num_workers, size_t* workspace_bytes) {
+  kvq_status st = check_layer(ctx, layer);
+  if (st != KVQ_OK) return st;
+  if (ctx->window[layer] != 0) return KVQ_ERR_UNSUPPORTED;
+  if (!num_workers || *num_workers < 0) return KVQ_ERR_INVALID_ARG;
+  st = kvq_decode_plan(ctx, layer, batch, max_context, num_workers, nullptr);
+  if (st != KVQ_OK) return st;
+  const kvq_config& c = ctx->cfg;
+  // partials, the rows' log2 sums, and the scores
+  if (workspace_bytes)
+    *workspace_bytes = partial_bytes(c, batch, *num_workers) +
+                       align16((size_t)batch * c.num_q_heads * sizeof(float)) +
+                       (size_t)batch * c.num_q_heads * (size_t)max_context * sizeof(float);
+  return KVQ_OK;
+}
+
+kvq_status kvq_decode_attention_weights(const kvq_ctx* ctx, int layer, const void* q,
+                                        const void* k_cache, const void* v_cache,
+                                        const float* k_scale, const float* v_scale,
+                                        const float* k_cache_scale, const float* v_cache_scale,
+                                        const int* block_table, int max_blocks_per_seq,
+                                        const int* context_lens, int batch, int max_context,
+                                        void* out, float decay, float* weights,
+                                        long long weights_stride, int num_workers,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  int workers = num_workers;
+  size_t need = 0;
+  kvq_status st = kvq_decode_weights_plan(ctx, layer, batch, max_context, &workers, &need);
+  if (st != KVQ_OK) return st;
+  if (max_blocks_per_seq < 0 || weights_stride < max_context || !(decay >= 0.f && decay <= 1.f))
+    return KVQ_ERR_INVALID_ARG;
+  if (batch == 0) return KVQ_OK;
+  const kvq_config& c = ctx->cfg;
+  // the second pass has a grid of (parts of the context, KV heads, sequences)
+  if (batch > 65535 || c.num_kv_heads > 65535 || workers > kMostWorkers) return KVQ_ERR_INVALID_ARG;
+  DecodeArgs a;
+  st = decode_args(ctx, layer, q, k_cache, v_cache, k_scale, v_scale, k_cache_scale, v_cache_scale,
+                   block_table, max_blocks_per_seq, context_lens, batch, max_context, out, &a);
+  if (st != KVQ_OK) return st;
+  if (!weights) return KVQ_ERR_INVALID_ARG;
+  if (!aligned4(weights)) return KVQ_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < need) return KVQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
+  a.err = error_word();
+  if (!a.err) return KVQ_ERR_CUDA;
+  a.workers = workers;
+  a.cap = max_context;                          // the scores' rows
+  a.stream_once = stream_once(ctx, layer, batch, max_context);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  place_partials(c, &a, ws);
+  ws += partial_bytes(c, batch, workers);
+  a.lse = reinterpret_cast<float*>(ws);
+  a.scores = reinterpret_cast<float*>(ws + align16((size_t)batch * c.num_q_heads * sizeof(float)));
+  return cuda_status(launch_decode_weights(ctx->mode[layer], c.head_dim,
+                                           c.num_q_heads / c.num_kv_heads, a, weights,
+                                           weights_stride, decay, static_cast<cudaStream_t>(stream)));
 }
 
 // ---------------------------------------------------------------- eviction

@@ -179,7 +179,7 @@ cudaError_t claunch(const PrefillArgs& pa, cudaStream_t st) {
   const long long grid = (long long)pa.qtiles * pa.splits * a.B * a.Hkv;
   kern<<<(unsigned)grid, WRoles<MODE, D, FEW>::THREADS, C::SMEM, st>>>(pa, km, vm);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || pa.splits <= 1) return e;
+  if (e != cudaSuccess || pa.splits <= 1 || pa.shared) return e;
   const long long items = (long long)a.B * pa.max_query * a.Hq;
   // its launch overlaps the attention's tail
   const int wpr = pa.splits <= 8 ? 1 : (pa.splits <= 16 ? 2 : (pa.splits <= 32 ? 4 : 8));
@@ -216,9 +216,12 @@ int cross_query_tile(int D, int G) {
   return (D == 256 ? WRoles<BF16, 256, false>::NQ : WRoles<BF16, 128, false>::NQ) * (WROWS / G);
 }
 
-cudaError_t launch_cross(int mode, int D, int G, const DecodeArgs& a, const int* query_start,
-                         int max_query_len, int splits, int split_tiles, cudaStream_t st) {
+namespace {
+
+cudaError_t launch(int mode, int D, int G, const DecodeArgs& a, const int* query_start,
+                   int max_query_len, int splits, int split_tiles, int shared, cudaStream_t st) {
   PrefillArgs pa = {};
+  pa.shared = shared;
   pa.d = a;
   pa.query_start = query_start;
   const int tile = cross_query_tile(D, G);
@@ -235,6 +238,18 @@ cudaError_t launch_cross(int mode, int D, int G, const DecodeArgs& a, const int*
     case INT4_PER_TOKEN_HEAD: return claunch_d<INT4_PER_TOKEN_HEAD>(D, pa, st);
     default: return cudaErrorInvalidValue;
   }
+}
+
+}  // namespace
+
+cudaError_t launch_cross(int mode, int D, int G, const DecodeArgs& a, const int* query_start,
+                         int max_query_len, int splits, int split_tiles, cudaStream_t st) {
+  return launch(mode, D, G, a, query_start, max_query_len, splits, split_tiles, 0, st);
+}
+
+cudaError_t launch_prefix(int mode, int D, int G, const DecodeArgs& a, const int* group_start,
+                          int max_group, int splits, int split_tiles, cudaStream_t st) {
+  return launch(mode, D, G, a, group_start, max_group, splits, split_tiles, 1, st);
 }
 
 }  // namespace kvq

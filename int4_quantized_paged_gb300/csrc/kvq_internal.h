@@ -55,6 +55,12 @@ struct DecodeArgs {
   int stream_once;             // pages larger than L2: copy them evict-first
   long long num_blocks;
   float qk_scale;              // softmax_scale * log2(e)
+  long long cap;               // decode: positions of a sequence that are read at most
+  // decode with accumulated weights
+  float* scores;               // [B][Hkv][cap][G], log2 units
+  float* lse;                  // [B][Hq] log2 of a row's weight sum
+  // decode behind a shared prefix
+  const int* first;            // [B] first position that is the sequence's own
 };
 
 enum RopeLayout { ROPE_HALF = 0, ROPE_INTERLEAVED = 1 };
@@ -144,6 +150,19 @@ struct EvictArgs {
   int seg_max;                 // set by the launcher: cells of a CTA at most
 };
 
+// Decode behind shared prefixes (beside DecodeArgs).
+struct SharedArgs {
+  const int* group_start;      // [groups + 1] rows of each group
+  const int* shared_lens;      // [groups]
+  int groups, max_group;
+  int splits, split_tiles;     // of the prefixes, as for the cross attention
+  int* first;                  // [B] where a row's own positions begin
+  int* group_of;               // [B] its group, -1: nothing shared
+  int* prefix;                 // [groups] positions that the group shares
+  float* o;                    // [splits][groups][max_group][Hq][D]
+  float* lse;                  // [splits][groups][max_group][Hq]
+};
+
 // Launchers (return cudaGetLastError() of the launch).
 cudaError_t launch_cache_write(int mode, int D, const WriteArgs& a, cudaStream_t st);
 cudaError_t launch_rope(int mode, int D, int layout, RopeArgs a, const RopeTable& tab,
@@ -203,6 +222,15 @@ cudaError_t launch_prompt(int D, const PromptArgs& a, long long q_stride, const 
 // CTAs per (row, KV head) of an eviction; 0: no cluster holds max_len weights.
 int evict_cluster(int max_len, long long items);
 cudaError_t launch_evict(EvictArgs a, int n, cudaStream_t st);
+
+// The cross attention's kernel with partial results only: the groups' rows against
+// the first prefix positions of their first row (context_lens: the prefixes).
+cudaError_t launch_prefix(int mode, int D, int G, const DecodeArgs& a, const int* group_start,
+                          int max_group, int splits, int split_tiles, cudaStream_t st);
+cudaError_t launch_shared(int mode, int D, int G, const DecodeArgs& a, const SharedArgs& x,
+                          cudaStream_t st);
+cudaError_t launch_decode_weights(int mode, int D, int G, const DecodeArgs& a, float* weights,
+                                  long long stride, float decay, cudaStream_t st);
 
 // Device error word of the current device.
 unsigned* error_word();

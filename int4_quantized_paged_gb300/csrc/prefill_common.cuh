@@ -18,6 +18,9 @@ struct PrefillArgs {
   int max_query;                 // the caller's bound of a sequence's queries
   int splits;                    // splits of a sequence's keys, at most
   int split_tiles;               // key tiles (of 64) per split; the last takes what is left
+  // the sequences are groups of rows that share a prefix: the pages are those of the
+  // group's first row, and every split leaves a partial
+  int shared;
 };
 
 // 16 raw code bytes -> their f16 (bf16 for BF16) values: 8 (BF16), 16 (FP8)

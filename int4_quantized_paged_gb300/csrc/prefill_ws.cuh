@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
   int n_b = pa.query_start[b + 1] - q0;
   const int L = a.context_lens[b];
   if constexpr (CROSS) {
+    if (pa.shared && L <= 0) return;                        // nothing shared: its rows are others' work
     if (n_b > pa.max_query) {                               // rows past the caller's bound
       if (tid == 0) atomicOr(a.err, ERR_BAD_INDEX);
       n_b = pa.max_query;
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
     const int ts = split * pa.split_tiles;
     if (ts >= tiles) return;
     const bool last = split == pa.splits - 1;
-    whole = pa.splits <= 1 || tiles <= pa.split_tiles;
+    whole = !pa.shared && (pa.splits <= 1 || tiles <= pa.split_tiles);
     kmin = ts * WKT;
     pmax = (last ? L : min(L, (ts + pa.split_tiles) * WKT)) - 1;
     first = pmax;                                           // every row sees the same keys
@@ -485,7 +486,8 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
         const int pt = 32 * c + lane;
         const int pos = t0 * WKT + 16 * pt;
         if (pt >= SUB * ntl || pos + 16 <= kmin || pos > pmax) return -1;
-        const int blk = __ldg(a.block_table + (long long)b * a.max_blocks + (pos >> a.bs_shift));
+        const int row = CROSS && pa.shared ? q0 : b;
+        const int blk = __ldg(a.block_table + (long long)row * a.max_blocks + (pos >> a.bs_shift));
         if (blk >= 0 && blk < a.num_blocks) return blk;
         atomicOr(a.err, ERR_BAD_INDEX);
         return -1;

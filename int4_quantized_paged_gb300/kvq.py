@@ -89,6 +89,13 @@ _SIGS = {
                                   P, sz, P]),
     "kvq_cross_plan": (i32, [P, i32, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(sz)]),
     "kvq_prompt_attention": (i32, [P, i32, P, i64, P, P, i64, P, i32, i32, i64, P, P]),
+    "kvq_shared_prefix_plan": (i32, [P, i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32),
+                                     ctypes.POINTER(sz)]),
+    "kvq_shared_prefix_attention": (i32, [P, i32, P, P, P, P, P, P, P, P, i32, P, i32, P, P, i32, i32,
+                                          i32, i32, P, i32, P, sz, P]),
+    "kvq_decode_weights_plan": (i32, [P, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(sz)]),
+    "kvq_decode_attention_weights": (i32, [P, i32, P, P, P, P, P, P, P, P, i32, P, i32, i32, P, f32, P,
+                                           i64, i32, P, sz, P]),
     "kvq_evict_cells": (i32, [P, i32, P, P, i32, i32, i32, P, P, i32, i32, P, i32, P, i64, P, P, P, P,
                               P, P]),
     "kvq_e4m3_encode": (i32, [P, P, i64, P]),
@@ -491,6 +498,65 @@ def kvq_prompt_attention(ctx: Context, layer: int, q, k, v, seq_start, out, *, m
     _check(_lib.kvq_prompt_attention(ctx.handle, layer, _ptr(q), q_token_stride, _ptr(k), _ptr(v),
                                      kv_token_stride, _ptr(seq_start), B, max_seq_len, T, _ptr(out),
                                      _stream(stream)), "kvq_prompt_attention")
+
+
+def kvq_shared_prefix_plan(ctx: Context, layer: int, batch: int, num_groups: int, *, max_group: int,
+                           max_shared: int, max_own: int, num_splits: int = 0):
+    """(splits of the prefixes, workspace bytes)."""
+    s, w = i32(num_splits), sz()
+    _check(_lib.kvq_shared_prefix_plan(ctx.handle, layer, batch, num_groups, max_group, max_shared, max_own,
+                                       ctypes.byref(s), ctypes.byref(w)), "kvq_shared_prefix_plan")
+    return s.value, w.value
+
+
+def kvq_shared_prefix_attention(ctx: Context, layer: int, q, k_cache, v_cache, block_table, context_lens,
+                                group_start, shared_lens, out, *, max_group: int, max_shared: int,
+                                max_own: int, k_scale=None, v_scale=None, k_cache_scale=None,
+                                v_cache_scale=None, num_splits: int = 0, workspace=None,
+                                workspace_bytes: Optional[int] = None, batch: Optional[int] = None,
+                                num_groups: Optional[int] = None,
+                                max_blocks_per_seq: Optional[int] = None, stream=None):
+    """Decode attention of groups of rows that share a prefix, which each group reads once; bf16
+    output; see include/kvq.h."""
+    B = q.shape[0] if batch is None else batch
+    NG = shared_lens.shape[0] if num_groups is None else num_groups
+    mb = block_table.shape[1] if max_blocks_per_seq is None else max_blocks_per_seq
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.kvq_shared_prefix_attention(
+        ctx.handle, layer, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(k_cache_scale), _ptr(v_cache_scale), _ptr(block_table), mb, _ptr(context_lens), B,
+        _ptr(group_start), _ptr(shared_lens), NG, max_group, max_shared, max_own, _ptr(out), num_splits,
+        _ptr(workspace), workspace_bytes, _stream(stream)), "kvq_shared_prefix_attention")
+
+
+def kvq_decode_weights_plan(ctx: Context, layer: int, batch: int, max_context: int, num_workers: int = 0):
+    """(worker warps, workspace bytes) of kvq_decode_attention_weights."""
+    n, w = i32(num_workers), sz()
+    _check(_lib.kvq_decode_weights_plan(ctx.handle, layer, batch, max_context, ctypes.byref(n),
+                                        ctypes.byref(w)), "kvq_decode_weights_plan")
+    return n.value, w.value
+
+
+def kvq_decode_attention_weights(ctx: Context, layer: int, q, k_cache, v_cache, block_table, context_lens,
+                                 weights, out, *, max_context: int, decay: float = 1.0, k_scale=None,
+                                 v_scale=None, k_cache_scale=None, v_cache_scale=None,
+                                 num_workers: int = 0, workspace=None,
+                                 workspace_bytes: Optional[int] = None, batch: Optional[int] = None,
+                                 max_blocks_per_seq: Optional[int] = None,
+                                 weights_stride: Optional[int] = None, stream=None):
+    """Decode attention with a bf16 output that adds each cell's softmax weight to weights (fp32
+    [batch, Hkv, stride]), the earlier sum times decay; see include/kvq.h."""
+    B = q.shape[0] if batch is None else batch
+    mb = block_table.shape[1] if max_blocks_per_seq is None else max_blocks_per_seq
+    ws = weights.shape[2] if weights_stride is None else weights_stride
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.kvq_decode_attention_weights(
+        ctx.handle, layer, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(k_cache_scale), _ptr(v_cache_scale), _ptr(block_table), mb, _ptr(context_lens), B, max_context,
+        _ptr(out), decay, _ptr(weights), ws, num_workers, _ptr(workspace), workspace_bytes,
+        _stream(stream)), "kvq_decode_attention_weights")
 
 
 def kvq_evict_cells(ctx: Context, layer: int, rows, keep_lens, block_table, context_lens, weights, new_lens,
