@@ -158,8 +158,8 @@ kvq_status kvq_prompt_attention(const kvq_ctx* ctx, int layer, const void* q,
     return KVQ_ERR_ALIGNMENT;
   const int G = c.num_q_heads / c.num_kv_heads;
   const long long most = max_seq_len < num_tokens ? max_seq_len : num_tokens;
-  const int per = prompt_positions_per_cta(c.head_dim, G);
-  if ((most + per - 1) / per * batch >= (1LL << 31) / c.num_kv_heads) return KVQ_ERR_INVALID_ARG;
+  if (prompt_items(c.head_dim, G, num_tokens, most, batch, 1) >= (1LL << 31) / c.num_kv_heads)
+    return KVQ_ERR_INVALID_ARG;
   unsigned* err = error_word();
   if (!err) return KVQ_ERR_CUDA;
   PromptArgs a = {};

@@ -131,7 +131,6 @@ struct PromptArgs {
   int B, Hq, Hkv, g_shift;     // 2^g_shift query heads per KV head
   int max_len;                 // the caller's bound of a sequence's length
   int window;
-  int qtiles;                  // set by the launcher: CTAs per (sequence, KV head)
   float qk_scale;              // softmax_scale * log2(e)
 };
 
@@ -215,7 +214,7 @@ cudaError_t launch_cross(int mode, int D, int G, const DecodeArgs& a, const int*
 bool make_rows_map(CUtensorMap* m, const void* base, int D, int heads, long long tokens,
                    long long stride, int box_heads, int box_tokens);
 
-int prompt_positions_per_cta(int D, int G);
+long long prompt_items(int D, int G, long long T, long long max_len, long long B, int Hkv);
 cudaError_t launch_prompt(int D, const PromptArgs& a, long long q_stride, const void* k, const void* v,
                           long long kv_stride, cudaStream_t st);
 

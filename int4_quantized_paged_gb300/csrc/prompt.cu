@@ -11,11 +11,17 @@
 // MMA have one type, and v is bf16), off by 2^-9 of itself on average and 2^-8 at
 // most, like the output's own rounding.
 //
-// Structure.  A CTA owns NQ query tiles of 128 rows (128 / G consecutive positions
-// times the G heads of one KV head, so that a tile's rows see almost the same keys)
-// and streams the keys up to its last position in tiles of KT.  Roles:
-//  * producer warp: Q, then K and V tiles by TMA straight into their operand layouts
-//    (rows of 128 bytes, 128-byte swizzle) through one ring of slots;
+// Structure.  Persistent CTAs, one per SM, take items: NQ query tiles of 128 rows (128 / G
+// consecutive positions times the G heads of one KV head, so that a tile's rows see
+// almost the same keys) against the keys up to their last position, in tiles of KT.
+// The grid has a CTA for each item; those that run cancel the launch of others and
+// take their items (cluster launch control), so that the hardware hands out the
+// work and an item's first loads and scores run under the previous one's softmax and
+// epilogue.  Items go by falling position: the ones with the most keys come first.
+// Roles:
+//  * producer warp: finds the items among the ragged sequences, loads Q, then K and V
+//    tiles by TMA straight into their operand layouts (rows of 128 bytes, 128-byte
+//    swizzle) through one ring of slots;
 //  * MMA warp, one elected lane: S_j = Q_j K^T into tensor memory and O_j += P_j V
 //    with P_j read from tensor memory, where it replaces S_j.  With two query tiles
 //    the order is PV_0, S_0, PV_1, S_1, so that the tensor cores work on one tile
@@ -25,7 +31,7 @@
 // A CTA's MMAs run in the order of their issue, so S_j(i + 1) may be issued behind
 // the PV_j(i) that still reads P from the same columns.
 //
-// Nothing beyond a CTA's last position is multiplied: the last key tile's MMAs
+// Nothing beyond an item's last position is multiplied: the last key tile's MMAs
 // stop at the 16 keys that hold it, and the V rows between it and their end are set
 // to zero, so that rows behind a sequence (of another one, or of none) may hold
 // anything, NaN too.
@@ -54,14 +60,21 @@ struct Shape {
   static constexpr int NB = D / 64;                        // 64-d blocks of a row
   static constexpr int QB = ROWS * D * 2;                  // bytes of a query tile
   static constexpr int SLOT = KT * D * 2;                  // and of a K or V tile
-  static constexpr int LIMIT = 232448 - 1024 - 512;        // shared memory, less alignment and barriers
-  static constexpr int NS = (LIMIT - NQ * QB) / SLOT < 8 ? (LIMIT - NQ * QB) / SLOT : 8;
-  static constexpr int SMEM = NQ * QB + NS * SLOT + 512 + 1024;
+  static constexpr int AUX = 512;                          // items and barriers
   static constexpr int SOFT = 4 * NQ;                      // softmax warps
+  static constexpr int OUT = SOFT * 32 * 128;              // 64 elements of their rows on the way out
+  static constexpr int LIMIT = 232448 - 1024 - AUX - OUT;  // shared memory, less alignment
+  static constexpr int NS = (LIMIT - NQ * QB) / SLOT < 8 ? (LIMIT - NQ * QB) / SLOT : 8;
+  static constexpr int SMEM = NQ * QB + NS * SLOT + OUT + AUX + 1024;
   static constexpr int PROD = SOFT, MMA = SOFT + 1;
   static constexpr int THREADS = (SOFT + 4) * 32;
   __host__ __device__ static constexpr int scol(int j, int b) { return NQ == 2 ? 128 * j : 256 + KT * b; }
   __host__ __device__ static constexpr int ocol(int j) { return NQ == 2 ? 256 + D * j : 0; }
+  // Two query tiles: the softmax warpgroups, whose threads hold 128 scores, take
+  // registers from the third one.  The shares are what the block is launched with.
+  static constexpr bool MOVE_REGS = NQ == 2;
+  static constexpr int REGS = 168, REGS_SOFT = 208, REGS_REST = 88;
+  static_assert(!MOVE_REGS || (2 * REGS_SOFT + REGS_REST == 3 * REGS && THREADS == 384), "register shares");
   static_assert(NS >= 4, "K and V of one tile in use, of the next under way");
 };
 
@@ -71,14 +84,33 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-__device__ __forceinline__ void store_bf16(uint16_t* row, const float (&v)[32], float f) {
-  uint4* dst = reinterpret_cast<uint4*>(row);
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    dst[e] = make_uint4(pack_bf16x2(v[8 * e] * f, v[8 * e + 1] * f),
-                        pack_bf16x2(v[8 * e + 2] * f, v[8 * e + 3] * f),
-                        pack_bf16x2(v[8 * e + 4] * f, v[8 * e + 5] * f),
-                        pack_bf16x2(v[8 * e + 6] * f, v[8 * e + 7] * f));
+// What a CTA works on: positions [p0, end) of the sequence that starts at token t0,
+// KV head g; p0 < 0: nothing is left.
+struct Item {
+  int t0, p0, end, g;
+};
+
+// Asks for the launch of one more CTA to be cancelled in favour of this one: 16 bytes
+// of answer, which complete on `bar`.
+__device__ __forceinline__ void ask_for_item(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::
+          "r"(smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The block index whose launch was cancelled, or -1: none was left.
+__device__ __forceinline__ long long read_answer(const void* answer) {
+  uint32_t ok, x;
+  asm volatile(
+      "{ .reg .b128 r; .reg .pred p; .reg .b32 y, z, w; ld.shared.b128 r, [%2];"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r; selp.u32 %0, 1, 0, p; mov.u32 %1, 0;"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r; }"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return ok ? (long long)x : -1;
 }
 
 template <int D>
@@ -92,67 +124,114 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
                                              ~uintptr_t(1023));
   uint8_t* qsm = smem;                                     // NQ query tiles
   uint8_t* ring = smem + NQ * C::QB;                       // NS slots
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + NS * C::SLOT);
+  uint8_t* outs = ring + NS * C::SLOT;                     // 4 KB per softmax warp
+  uint8_t* answer = outs + C::OUT;                         // 16 bytes
+  volatile Item* items = reinterpret_cast<volatile Item*>(answer + 16);   // [2]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(answer + 48);
   uint64_t* full = bars;                                   // [NS] producer -> MMA
   uint64_t* empty = full + NS;                             // [NS] MMA (commit) -> producer
-  uint64_t* q_full = empty + NS;
-  uint64_t* s_full = q_full + 1;                           // [NQ][SB] MMA (commit) -> softmax
+  uint64_t* asked = empty + NS;                            // the answer is there
+  uint64_t* item_full = asked + 1;                         // [2] producer -> MMA, softmax
+  uint64_t* item_empty = item_full + 2;                    // [2] MMA, softmax -> producer
+  uint64_t* q_full = item_empty + 2;                       // producer -> MMA
+  uint64_t* q_empty = q_full + 1;                          // MMA (commit) -> producer
+  uint64_t* s_full = q_empty + 1;                          // [NQ][SB] MMA (commit) -> softmax
   uint64_t* p_full = s_full + NQ * SB;                     // [NQ][SB] softmax -> MMA
   uint64_t* pv_done = p_full + NQ * SB;                    // [NQ][SB] MMA (commit) -> softmax
-  uint64_t* o_full = pv_done + NQ * SB;                    // [NQ] MMA (commit), after the last PV
-  uint64_t* fin = o_full + NQ;                             // the MMA warp's own end
-  static_assert((2 * NS + 1 + 3 * NQ * SB + NQ + 2) * 8 <= 512, "barriers");
+  uint64_t* o_full = pv_done + NQ * SB;                    // [NQ] MMA (commit), an item's last PV
+  uint64_t* o_empty = o_full + NQ;                         // [NQ] softmax -> MMA
+  uint64_t* fin = o_empty + NQ;                            // the MMA warp's own end
+  static_assert(48 + (2 * NS + 8 + 3 * NQ * SB + 2 * NQ + 2) * 8 <= C::AUX, "barriers");
   volatile int* s_abort = reinterpret_cast<volatile int*>(fin + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(fin + 1) + 1;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-
-  // ---- this CTA's sequence, KV head and query tiles; the longest rows of keys first
-  const int per_tile = a.B * a.Hkv;
-  const int ct = a.qtiles - 1 - (int)(blockIdx.x / per_tile);
-  const int rem = (int)(blockIdx.x % per_tile);
-  const int b = rem / a.Hkv, g = rem - b * a.Hkv;
   const int QP = ROWS >> a.g_shift;                        // positions per query tile
-  const int t0 = a.seq_start[b];
-  int n = a.seq_start[b + 1] - t0;
-  const bool bad = t0 < 0 || n < 0 || (long long)t0 + n > a.T;
-  if (bad || n > a.max_len) {
-    if (tid == 0) atomicOr(a.err, ERR_BAD_INDEX);
-    if (bad) return;
-    n = a.max_len;                                         // rows past the caller's bound
-  }
-  const int p0 = ct * NQ * QP;                             // first position here
-  if (p0 >= n) return;                                     // whole CTA: before any barrier
-  const int end = min(n, p0 + NQ * QP);                    // behind the last position
-  const int nqt = end - p0 <= QP ? 1 : NQ;                 // query tiles with rows in use
-  const int first_key = a.window > 0 ? max(0, p0 + 1 - a.window) : 0;
-  const int kt0 = first_key / KT;                          // first key tile
-  auto tile_end = [&](int j) { return min(end, p0 + (j + 1) * QP); };
-  auto tiles_of = [&](int j) { return (tile_end(j) + KT - 1) / KT - kt0; };
-  const int ntl = tiles_of(nqt - 1);                       // key tiles of the CTA
+  const int per = NQ * QP;                                 // and per item
 
-  if (warp == C::PROD && elect_one()) {
-    prefetch_map(&qmap);
-    prefetch_map(&kmap);
-    prefetch_map(&vmap);
+  // ---- the producer's view of the sequences: item w of the list, by levels.  Level q
+  // has an item for each KV head of each sequence that is longer than q * per.
+  auto length = [&](int b) -> int {
+    if (b >= a.B) return 0;
+    const int t = a.seq_start[b], n = a.seq_start[b + 1] - t;
+    const bool bad = t < 0 || n < 0 || (long long)t + n > a.T;
+    if (blockIdx.x == 0 && (bad || n > a.max_len)) atomicOr(a.err, ERR_BAD_INDEX);
+    return bad ? 0 : min(n, a.max_len);                    // tokens past the caller's bound
+  };
+  int n0 = 0, level = 0, at_level = 0;                     // lengths of the first 32; level, its sequences
+  long long before = 0;                                    // items of the levels above
+  auto longer = [&](int b0, int than) -> unsigned {        // sequences b0 + bit
+    const int n = b0 == 0 ? n0 : length(b0 + lane);
+    return __ballot_sync(0xffffffffu, n > than);
+  };
+  auto find = [&](long long w) -> Item {
+    Item it = {0, -1, 0, 0};
+    while (w >= before + (long long)at_level * a.Hkv) {
+      before += (long long)at_level * a.Hkv;
+      if (--level < 0) return it;
+      at_level = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) at_level += __popc(longer(b0, level * per));
+    }
+    int r = (int)(w - before) / a.Hkv;                     // which of the level's sequences
+    it.g = (int)(w - before) - r * a.Hkv;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const unsigned m = longer(b0, level * per);
+      const int here = __popc(m);
+      if (r < here) {
+        const bool me = ((m >> lane) & 1u) && __popc(m & ((1u << lane) - 1u)) == r;
+        const int b = b0 + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+        it.t0 = a.seq_start[b];
+        it.p0 = level * per;
+        it.end = min(min(a.seq_start[b + 1] - it.t0, a.max_len), it.p0 + per);
+        return it;
+      }
+      r -= here;
+    }
+    return it;
+  };
+
+  Item first = {0, -1, 0, 0};
+  if (warp == C::PROD) {
+    if (elect_one()) {
+      prefetch_map(&qmap);
+      prefetch_map(&kmap);
+      prefetch_map(&vmap);
+    }
+    n0 = length(lane);
+    int most = n0;
+    for (int b0 = 32; b0 < a.B; b0 += 32) most = max(most, length(b0 + lane));
+    most = __reduce_max_sync(0xffffffffu, most);
+    level = (most + per - 1) / per;
+    first = find(blockIdx.x);
+    if (lane == 0) *s_abort = first.p0 < 0;
   }
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
+    mbar_init(asked, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&item_full[s], 1);
+      mbar_init(&item_empty[s], C::SOFT + 1);
+    }
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     for (int s = 0; s < NQ * SB; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 128);
       mbar_init(&pv_done[s], 1);
     }
-    for (int j = 0; j < NQ; ++j) mbar_init(&o_full[j], 1);
+    for (int j = 0; j < NQ; ++j) {
+      mbar_init(&o_full[j], 1);
+      mbar_init(&o_empty[j], 4);
+    }
     mbar_init(fin, 1);
     mbar_init_fence();
-    *s_abort = 0;
   }
+  __syncthreads();
+  if (*s_abort) return;                                    // no item here: the whole CTA
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(s_tmem)),
@@ -170,241 +249,374 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
     if (!ok && lane == 0) { *s_abort = 1; atomicOr(a.err, ERR_TIMEOUT); }
     return ok && !__any_sync(0xffffffffu, *s_abort);
   };
+  // Item k of this CTA, for the MMA and softmax warps; false when there is none.
+  auto take_item = [&](int k, Item& it) -> bool {
+    if (!wait(&item_full[k & 1], (uint32_t)((k >> 1) & 1))) return false;
+    // through shuffles: the compiler then knows what follows from an item to be
+    // warp-uniform, as a role's loops and descriptors are
+    volatile Item* i = items + (k & 1);
+    it.t0 = __shfl_sync(0xffffffffu, i->t0, 0);
+    it.p0 = __shfl_sync(0xffffffffu, i->p0, 0);
+    it.end = __shfl_sync(0xffffffffu, i->end, 0);
+    it.g = __shfl_sync(0xffffffffu, i->g, 0);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+    return it.p0 >= 0;
+  };
+  // Key tiles of an item: from first_tile on, tiles_of(j) for query tile j.
+  auto first_tile = [&](const Item& it) { return a.window > 0 ? max(0, it.p0 + 1 - a.window) / KT : 0; };
+  auto query_tiles = [&](const Item& it) { return it.end - it.p0 <= QP ? 1 : NQ; };
+  auto tile_end = [&](const Item& it, int j) { return min(it.end, it.p0 + (j + 1) * QP); };
+  auto tiles_of = [&](const Item& it, int j) { return (tile_end(it, j) + KT - 1) / KT - first_tile(it); };
 
   // ================================================================ roles
-  if (warp == C::PROD) {
-    // ---- producer: the ring's order is K(0 .. SB-1), then V(i), K(i + SB)
-    int issued = 0;
-    auto load = [&](const CUtensorMap* map, int tile) -> bool {
-      const int slot = issued % NS;
-      if (issued >= NS && !wait(&empty[slot], (uint32_t)((issued / NS - 1) & 1))) return false;
-      if (elect_one()) {
-        mbar_expect_tx(&full[slot], C::SLOT);
+  if (warp >= C::SOFT) {
+    if constexpr (C::MOVE_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_REST));
+    if (warp == C::PROD) {
+      // ---- producer: the ring's order is K(0 .. SB-1), then V(i), K(i + SB)
+      int issued = 0, k = 0;
+      Item it = first;
+      auto load = [&](const CUtensorMap* map, int key) -> bool {
+        const int slot = issued % NS;
+        if (issued >= NS && !wait(&empty[slot], (uint32_t)((issued / NS - 1) & 1))) return false;
+        if (elect_one()) {
+          mbar_expect_tx(&full[slot], C::SLOT);
 #pragma unroll
-        for (int c = 0; c < C::NB; ++c)
-          tma_tile_3d(ring + slot * C::SLOT + c * (KT * 128), map, 128 * c, g, t0 + (kt0 + tile) * KT,
-                      &full[slot]);
-      }
-      __syncwarp();
-      ++issued;
-      return true;
-    };
-    if (elect_one()) {
-      mbar_expect_tx(q_full, nqt * C::QB);
-      for (int j = 0; j < nqt; ++j)
-#pragma unroll
-        for (int c = 0; c < C::NB; ++c)
-          tma_tile_3d(qsm + j * C::QB + c * (ROWS * 128), &qmap, 128 * c, g << a.g_shift, t0 + p0 + j * QP,
-                      q_full);
-    }
-    __syncwarp();
-    bool go = true;
-    for (int i = 0; go && i < SB && i < ntl; ++i) go = load(&kmap, i);
-    for (int i = 0; go && i < ntl; ++i) {
-      go = load(&vmap, i);
-      if (go && i + SB < ntl) go = load(&kmap, i + SB);
-    }
-    // every copy has landed before the CTA exits
-    (void)mbar_wait(q_full, 0u);
-    for (int x = max(0, issued - NS); x < issued; ++x)
-      (void)mbar_wait(&full[x % NS], (uint32_t)((x / NS) & 1));
-  } else if (warp == C::MMA) {
-    // ---- MMA issuer
-    const uint64_t dq = sw128_desc(qsm), dk = sw128_desc(ring), dv = sw128_mn_desc(ring, KT * 128);
-    // keys of key tile i that query tile j multiplies, a multiple of 16
-    auto keys_of = [&](int j, int i) {
-      return min(KT, (tile_end(j) - (kt0 + i) * KT + 15) & ~15);
-    };
-    auto issue_s = [&](int j, int i, int slot) {
-      const uint64_t qa = dq + (uint64_t)(j * (C::QB >> 4));
-      const uint64_t kb = dk + (uint64_t)(slot * (C::SLOT >> 4));
-      const uint32_t td = tmem + C::scol(j, i % SB);
-      const uint32_t id = mma_idesc<true>(ROWS, keys_of(j, i));
-      if (elect_one()) {
-        tc_fence_after();
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          umma(td, qa + (uint64_t)((((s >> 2) * (ROWS * 128)) + (s & 3) * 32) >> 4),
-               kb + (uint64_t)((((s >> 2) * (KT * 128)) + (s & 3) * 32) >> 4), id, s > 0);
-        umma_commit(&s_full[j * SB + i % SB]);
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](int j, int i, int slot) {
-      const uint64_t vb = dv + (uint64_t)(slot * (C::SLOT >> 4));
-      const uint32_t td = tmem + C::ocol(j), ta = tmem + C::scol(j, i % SB);
-      const int steps = keys_of(j, i) / 16;
-      constexpr uint32_t id = mma_idesc<true>(ROWS, D) | MMA_B_MN_MAJOR;
-      if (elect_one()) {
-        tc_fence_after();
-        for (int s = 0; s < steps; ++s)
-          umma_tmem_a(td, ta + 8 * s, vb + (uint64_t)(s * (16 * 128 >> 4)), id, i > 0 || s > 0);
-        umma_commit(i == tiles_of(j) - 1 ? &o_full[j] : &pv_done[j * SB + i % SB]);
-      }
-      __syncwarp();
-    };
-    auto release = [&](int slot) {
-      if (elect_one()) umma_commit(&empty[slot]);
-      __syncwarp();
-    };
-    int x = 0;                                             // next entry of the ring
-    auto take = [&](int& slot) -> bool {
-      slot = x % NS;
-      const bool ok = wait(&full[slot], (uint32_t)((x / NS) & 1));
-      ++x;
-      return ok;
-    };
-    bool go = wait(q_full, 0u);
-    int slot = 0;
-    for (int i = 0; go && i < SB && i < ntl; ++i) {
-      go = take(slot);
-      if (!go) break;
-      for (int j = 0; j < nqt; ++j)
-        if (i < tiles_of(j)) issue_s(j, i, slot);
-      release(slot);
-    }
-    for (int i = 0; go && i < ntl; ++i) {
-      int vslot = 0, kslot = 0;
-      go = take(vslot);
-      if (!go) break;
-      if (i == ntl - 1) {
-        // rows between the CTA's last position and the end of its 16 keys
-        const int from = end - (kt0 + i) * KT, to = (from + 15) & ~15;
-        uint8_t* v = ring + vslot * C::SLOT;
-        for (int e = lane; e < (to - from) * (D / 8); e += 32) {
-          const int row = from + e / (D / 8), c = e % (D / 8);
-          *reinterpret_cast<uint4*>(v + (c >> 3) * (KT * 128) + row * 128 + ((c & 7) << 4)) =
-              make_uint4(0u, 0u, 0u, 0u);
+          for (int c = 0; c < C::NB; ++c)
+            tma_tile_3d(ring + slot * C::SLOT + c * (KT * 128), map, 128 * c, it.g, it.t0 + key, &full[slot]);
         }
-        fence_proxy_async();
         __syncwarp();
-      }
-      const bool more = i + SB < ntl;
-      bool have_k = false;
-      for (int j = 0; go && j < nqt; ++j) {
-        if (i >= tiles_of(j)) continue;
-        go = wait(&p_full[j * SB + i % SB], (uint32_t)((i / SB) & 1));
+        ++issued;
+        return true;
+      };
+      auto publish = [&]() -> bool {
+        if (k >= 2 && !wait(&item_empty[k & 1], (uint32_t)(((k >> 1) - 1) & 1))) return false;
+        if (lane == 0) {
+          volatile Item* i = items + (k & 1);
+          i->t0 = it.t0;
+          i->p0 = it.p0;
+          i->end = it.end;
+          i->g = it.g;
+          mbar_arrive(&item_full[k & 1]);
+        }
+        __syncwarp();
+        return true;
+      };
+      int loaded = 0;                                      // items whose Q was loaded
+      for (bool go = publish(); go && it.p0 >= 0; go = publish()) {
+        const int nqt = query_tiles(it), kt0 = first_tile(it), ntl = tiles_of(it, nqt - 1);
+        for (int i = 0; go && i < SB && i < ntl; ++i) go = load(&kmap, (kt0 + i) * KT);
+        if (go && k >= 1) go = wait(q_empty, (uint32_t)((k - 1) & 1));
         if (!go) break;
-        issue_pv(j, i, vslot);
-        if (i + SB < tiles_of(j)) {
-          if (!have_k) go = take(kslot);
-          have_k = true;
-          if (go) issue_s(j, i + SB, kslot);
+        if (elect_one()) {
+          mbar_expect_tx(q_full, nqt * C::QB);
+          for (int j = 0; j < nqt; ++j)
+#pragma unroll
+            for (int c = 0; c < C::NB; ++c)
+              tma_tile_3d(qsm + j * C::QB + c * (ROWS * 128), &qmap, 128 * c, it.g << a.g_shift,
+                          it.t0 + it.p0 + j * QP, q_full);
+        }
+        __syncwarp();
+        ++loaded;
+        for (int i = 0; go && i < ntl; ++i) {
+          if (i == max(0, ntl - 2) && elect_one()) {       // the next item, no earlier than needed
+            mbar_expect_tx(asked, 16);
+            ask_for_item(answer, asked);
+          }
+          __syncwarp();
+          go = load(&vmap, (kt0 + i) * KT);
+          if (go && i + SB < ntl) go = load(&kmap, (kt0 + i + SB) * KT);
+        }
+        // the answer arrives in any case (and has to, before the CTA exits)
+        if (!wait(asked, (uint32_t)(k & 1)) || !go) break;
+        const long long w = read_answer(answer);
+        fence_proxy_async();                               // read before it is written again
+        __syncwarp();
+        it.p0 = -1;
+        if (w >= 0) it = find(w);
+        ++k;
+      }
+      // every copy has landed before the CTA exits
+      if (loaded > 0) (void)mbar_wait(q_full, (uint32_t)((loaded - 1) & 1));
+      for (int x = max(0, issued - NS); x < issued; ++x)
+        (void)mbar_wait(&full[x % NS], (uint32_t)((x / NS) & 1));
+    } else if (warp == C::MMA) {
+      // ---- MMA issuer
+      const uint64_t dq = sw128_desc(qsm), dk = sw128_desc(ring), dv = sw128_mn_desc(ring, KT * 128);
+      int x = 0;                                           // next entry of the ring
+      int used[NQ], items_of[NQ];                          // query tile j's key tiles and items so far
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) used[j] = items_of[j] = 0;
+      auto take = [&](int& slot) -> bool {
+        slot = x % NS;
+        const bool ok = wait(&full[slot], (uint32_t)((x / NS) & 1));
+        ++x;
+        return ok;
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) umma_commit(bar);
+        __syncwarp();
+      };
+      Item it;
+      bool go = true;
+      for (int k = 0; go && take_item(k, it); ++k) {
+        const int nqt = query_tiles(it), kt0 = first_tile(it), ntl = tiles_of(it, nqt - 1);
+        // key tiles of query tile j, and the keys of its last one, a multiple of 16
+        int nt[NQ], rest[NQ];
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+          nt[j] = j < nqt ? tiles_of(it, j) : 0;
+          rest[j] = min(KT, (tile_end(it, j) - (kt0 + nt[j] - 1) * KT + 15) & ~15);
+        }
+        auto issue_s = [&](int j, int i, int slot) {
+          const uint64_t qa = dq + (uint64_t)(j * (C::QB >> 4));
+          const uint64_t kb = dk + (uint64_t)(slot * (C::SLOT >> 4));
+          const int sb = (used[j] + i) % SB;
+          const uint32_t td = tmem + C::scol(j, sb);
+          const uint32_t id = mma_idesc<true>(ROWS, i == nt[j] - 1 ? rest[j] : KT);
+          if (elect_one()) {
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              umma(td, qa + (uint64_t)((((s >> 2) * (ROWS * 128)) + (s & 3) * 32) >> 4),
+                   kb + (uint64_t)((((s >> 2) * (KT * 128)) + (s & 3) * 32) >> 4), id, s > 0);
+            umma_commit(&s_full[j * SB + sb]);
+          }
+          __syncwarp();
+        };
+        auto issue_pv = [&](int j, int i, int slot) {
+          const uint64_t vb = dv + (uint64_t)(slot * (C::SLOT >> 4));
+          const int sb = (used[j] + i) % SB;
+          const uint32_t td = tmem + C::ocol(j), ta = tmem + C::scol(j, sb);
+          const bool last = i == nt[j] - 1;
+          constexpr uint32_t id = mma_idesc<true>(ROWS, D) | MMA_B_MN_MAJOR;
+          if (elect_one()) {
+            tc_fence_after();
+            if (last) {
+              for (int s = 0; s < rest[j] / 16; ++s)
+                umma_tmem_a(td, ta + 8 * s, vb + (uint64_t)(s * (16 * 128 >> 4)), id, i > 0 || s > 0);
+            } else {
+#pragma unroll
+              for (int s = 0; s < KT / 16; ++s)
+                umma_tmem_a(td, ta + 8 * s, vb + (uint64_t)(s * (16 * 128 >> 4)), id, i > 0 || s > 0);
+            }
+            if constexpr (SB > 1) umma_commit(&pv_done[j * SB + sb]);
+            if (last) umma_commit(&o_full[j]);
+          }
+          __syncwarp();
+        };
+        go = wait(q_full, (uint32_t)(k & 1));
+        int slot = 0;
+        for (int i = 0; go && i < SB && i < ntl; ++i) {
+          go = take(slot);
+          if (!go) break;
+#pragma unroll
+          for (int j = 0; j < NQ; ++j)
+            if (i < nt[j]) issue_s(j, i, slot);
+          commit(&empty[slot]);
+        }
+        if (go && ntl <= SB) commit(q_empty);
+        for (int i = 0; go && i < ntl; ++i) {
+          int vslot = 0, kslot = 0;
+          go = take(vslot);
+          if (!go) break;
+          if (i == ntl - 1) {
+            // rows between the item's last position and the end of its 16 keys
+            const int from = it.end - (kt0 + i) * KT, to = (from + 15) & ~15;
+            uint8_t* v = ring + vslot * C::SLOT;
+            for (int e = lane; e < (to - from) * (D / 8); e += 32) {
+              const int row = from + e / (D / 8), c = e % (D / 8);
+              *reinterpret_cast<uint4*>(v + (c >> 3) * (KT * 128) + row * 128 + ((c & 7) << 4)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async();
+            __syncwarp();
+          }
+          const bool more = i + SB < ntl;
+          bool have_k = false;
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) {
+            if (!go || i >= nt[j]) continue;
+            const int u = used[j] + i;
+            // O_j of the item before has been read
+            if (i == 0 && items_of[j] > 0) go = wait(&o_empty[j], (uint32_t)((items_of[j] - 1) & 1));
+            if (go) go = wait(&p_full[j * SB + u % SB], (uint32_t)((u / SB) & 1));
+            if (!go) continue;
+            issue_pv(j, i, vslot);
+            if (i + SB < nt[j]) {
+              if (!have_k) go = take(kslot);
+              have_k = true;
+              if (go) issue_s(j, i + SB, kslot);
+            }
+          }
+          if (!go) break;
+          commit(&empty[vslot]);
+          if (more) commit(&empty[kslot]);
+          if (i + SB == ntl - 1) commit(q_empty);          // the item's last scores
+        }
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+          used[j] += nt[j];
+          items_of[j] += j < nqt;
         }
       }
-      if (!go) break;
-      release(vslot);
-      if (more) release(kslot);
+      // what was issued completes before the CTA exits
+      commit(fin);
+      (void)mbar_wait(fin, 0u);
     }
-    // what was issued completes before the CTA exits
-    if (elect_one()) umma_commit(fin);
-    __syncwarp();
-    (void)mbar_wait(fin, 0u);
-  } else if (warp < C::SOFT && (warp >> 2) < nqt) {
+  } else {
+    if constexpr (C::MOVE_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
     // ---- softmax of query tile j
     const int j = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
-    const int pos = p0 + j * QP + (r >> a.g_shift);        // this row's position
-    const int lo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
-    const int jfirst = p0 + j * QP, jlast = tile_end(j) - 1;
+    const int off = j * QP + (r >> a.g_shift);             // this row's position within the item
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tO = trow + C::ocol(j);
     const float c = a.qk_scale;
-    float m = -INFINITY, l = 0.f;
+    int used = 0, items_done = 0;
     bool ok = true;
-    const int nt = tiles_of(j);
-    for (int i = 0; i < nt; ++i) {
-      const uint32_t tS = trow + C::scol(j, i % SB);
-      ok = wait(&s_full[j * SB + i % SB], (uint32_t)((i / SB) & 1));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t s[KT / 32][32];
+    Item it;
+    for (int k = 0; ok && take_item(k, it); ++k) {
+      if (j >= query_tiles(it)) continue;
+      const int kt0 = first_tile(it), nt = tiles_of(it, j);
+      const int pos = it.p0 + off;
+      const int lo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
+      const int jfirst = it.p0 + j * QP, jlast = tile_end(it, j) - 1;
+      // no row of this warp is in use: its P may stay what it is (rows of an MMA's A
+      // operand do not mix), and it only keeps the barriers' counts
+      const bool idle = __all_sync(0xffffffffu, pos >= it.end);
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < nt; ++i) {
+        const int u = used + i, sb = j * SB + u % SB;
+        const uint32_t tS = trow + C::scol(j, u % SB);
+        ok = wait(&s_full[sb], (uint32_t)((u / SB) & 1));
+        if (!ok) break;
+        if (idle) {
+          mbar_arrive(&p_full[sb]);
+          continue;
+        }
+        tc_fence_after();
+        uint32_t s[KT / 32][32];
 #pragma unroll
-      for (int q = 0; q < KT / 32; ++q) tmem_ld32_nowait(tS + 32 * q, s[q]);
-      tmem_wait_ld();
-      const int k0 = (kt0 + i) * KT;
-      // a tile that some row does not see whole
-      if (k0 + KT - 1 > jfirst || (a.window > 0 && k0 < jlast + 1 - a.window)) {
-        const int klo = lo - k0, khi = pos - k0;
+        for (int q = 0; q < KT / 32; ++q) tmem_ld32_nowait(tS + 32 * q, s[q]);
+        tmem_wait_ld();
+        const int k0 = (kt0 + i) * KT;
+        // a tile that some row does not see whole
+        if (k0 + KT - 1 > jfirst || (a.window > 0 && k0 < jlast + 1 - a.window)) {
+#pragma unroll
+          for (int q = 0; q < KT / 32; ++q) {
+            // a bit for each of 32 keys: a test per bit instead of two comparisons
+            const int klo = max(lo - k0 - 32 * q, 0), khi = min(pos - k0 - 32 * q, 31);
+            const uint32_t seen = klo > khi ? 0u : (0xffffffffu >> (31 - khi)) & (0xffffffffu << klo);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((seen >> e) & 1u)) s[q][e] = 0xFF800000u;   // -inf
+          }
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int q = 0; q < KT / 32; ++q)
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (32 * q + e < klo || 32 * q + e > khi) s[q][e] = 0xFF800000u;   // -inf
-      }
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          for (int e = 0; e < 32; e += 8)
 #pragma unroll
-      for (int q = 0; q < KT / 32; ++q)
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            m4[u] = max3(m4[u], __uint_as_float(s[q][e + 2 * u]), __uint_as_float(s[q][e + 2 * u + 1]));
-      const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
-      float al = 1.f;
-      if (top > m + LAZY || (m == -INFINITY && top > -INFINITY)) {
-        al = m == -INFINITY ? 0.f : ex2(m - top);
-        m = top;
-      }
-      l *= al;
-      if (i > 0 && __any_sync(0xffffffffu, al != 1.f)) {
-        // with one S buffer S(i) ran behind PV(i - 1), which is then done
-        if constexpr (SB > 1) {
-          ok = wait(&pv_done[j * SB + (i - 1) % SB], (uint32_t)(((i - 1) / SB) & 1));
-          if (!ok) break;
-          tc_fence_after();
+            for (int v = 0; v < 4; ++v)
+              m4[v] = max3(m4[v], __uint_as_float(s[q][e + 2 * v]), __uint_as_float(s[q][e + 2 * v + 1]));
+        const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+        float al = 1.f;
+        if (top > m + LAZY || (m == -INFINITY && top > -INFINITY)) {
+          al = m == -INFINITY ? 0.f : ex2(m - top);
+          m = top;
         }
+        l *= al;
+        if (i > 0 && __any_sync(0xffffffffu, al != 1.f)) {
+          // with one S buffer S(i) ran behind PV(i - 1), which is then done
+          if constexpr (SB > 1) {
+            ok = wait(&pv_done[j * SB + (u - 1) % SB], (uint32_t)(((u - 1) / SB) & 1));
+            if (!ok) break;
+            tc_fence_after();
+          }
 #pragma unroll 1
-        for (int d = 0; d < D; d += 32) {
-          float v[32];
-          tmem_ld32(tO + d, v);
+          for (int d = 0; d < D; d += 32) {
+            float v[32];
+            tmem_ld32(tO + d, v);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= al;
-          tmem_st32(tO + d, v);
+            for (int e = 0; e < 32; ++e) v[e] *= al;
+            tmem_st32(tO + d, v);
+          }
         }
-      }
-      const float ref = m == -INFINITY ? 0.f : m;
-      const uint64_t c2 = pack_f32x2(c, c), r2 = pack_f32x2(-ref, -ref);
-      uint64_t l01 = 0, l23 = 0;
+        const float ref = m == -INFINITY ? 0.f : m;
+        const uint64_t c2 = pack_f32x2(c, c), r2 = pack_f32x2(-ref, -ref);
+        uint64_t l01 = 0, l23 = 0;
 #pragma unroll
-      for (int q = 0; q < KT / 32; ++q) {
-        uint32_t w[16];
+        for (int q = 0; q < KT / 32; ++q) {
+          uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          float x[4];
-          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), c2, r2),
-                       x[0], x[1]);
-          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3])), c2, r2),
-                       x[2], x[3]);
+          for (int e = 0; e < 32; e += 4) {
+            float y[4];
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), c2, r2),
+                         y[0], y[1]);
+            unpack_f32x2(
+                fma_f32x2(pack_f32x2(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3])), c2, r2), y[2],
+                y[3]);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) x[u] = ex2(x[u]);
-          l01 = add_f32x2(l01, pack_f32x2(x[0], x[1]));
-          l23 = add_f32x2(l23, pack_f32x2(x[2], x[3]));
-          w[e / 2] = pack_bf16x2(x[0], x[1]);
-          w[e / 2 + 1] = pack_bf16x2(x[2], x[3]);
+            for (int v = 0; v < 4; ++v) y[v] = ex2(y[v]);
+            l01 = add_f32x2(l01, pack_f32x2(y[0], y[1]));
+            l23 = add_f32x2(l23, pack_f32x2(y[2], y[3]));
+            w[e / 2] = pack_bf16x2(y[0], y[1]);
+            w[e / 2 + 1] = pack_bf16x2(y[2], y[3]);
+          }
+          tmem_st16_nowait(tS + 16 * q, w);
         }
-        tmem_st16_nowait(tS + 16 * q, w);
+        float y[4];
+        unpack_f32x2(l01, y[0], y[1]);
+        unpack_f32x2(l23, y[2], y[3]);
+        l += (y[0] + y[1]) + (y[2] + y[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[sb]);
       }
-      float y[4];
-      unpack_f32x2(l01, y[0], y[1]);
-      unpack_f32x2(l23, y[2], y[3]);
-      l += (y[0] + y[1]) + (y[2] + y[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&p_full[j * SB + i % SB]);
-    }
-    // ---- epilogue: O / l
-    if (ok) ok = wait(&o_full[j], 0u);
-    if (ok) {
+      used += nt;
+      // ---- epilogue: O / l
+      if (ok) ok = wait(&o_full[j], (uint32_t)(items_done & 1));
+      if (!ok) break;
+      ++items_done;
       tc_fence_after();
       const float f = l > 0.f ? 1.f / l : 0.f;
-      const int h = (g << a.g_shift) + (r & ((1 << a.g_shift) - 1));
-      uint16_t* row = a.out + ((long long)(t0 + pos) * a.Hq + h) * D;
+      // The rows go out through shared memory, 64 elements at a time, so that eight
+      // lanes write 128 bytes of one row (a lane's own row is a line of its own for each
+      // lane: 32 lines a store, four to eight times the time)
+      uint8_t* mine = outs + warp * (32 * 128);
 #pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
-        float v[32];
-        tmem_ld32(tO + d, v);
-        if (pos < end) store_bf16(row + d, v, f);
+      for (int d = 0; d < D; d += 64) {
+        if (!idle) {
+          uint32_t v[2][32];
+          tmem_ld32_nowait(tO + d, v[0]);
+          tmem_ld32_nowait(tO + d + 32, v[1]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t* x = v[e >> 2] + 8 * (e & 3);
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              w[y] = pack_bf16x2(__uint_as_float(x[2 * y]) * f, __uint_as_float(x[2 * y + 1]) * f);
+            *reinterpret_cast<uint4*>(mine + swc(lane, e)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (d + 64 == D) tc_fence_before();
+        __syncwarp();
+        if (d + 64 == D && lane == 0) mbar_arrive(&o_empty[j]);
+        if (idle) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int row = 4 * e + (lane >> 3), R = (warp & 3) * 32 + row;
+          const int p = it.p0 + j * QP + (R >> a.g_shift);
+          const int h = (it.g << a.g_shift) + (R & ((1 << a.g_shift) - 1));
+          if (p < it.end)
+            *reinterpret_cast<uint4*>(a.out + ((long long)(it.t0 + p) * a.Hq + h) * D + d + 8 * (lane & 7)) =
+                *reinterpret_cast<const uint4*>(mine + swc(row, lane & 7));
+        }
+        __syncwarp();
       }
     }
   }
@@ -416,6 +628,17 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
 }
+
+}  // namespace
+
+// Sequences of n tokens have ceil(n / per) items each: at most this many in T tokens.
+long long prompt_items(int D, int G, long long T, long long max_len, long long B, int Hkv) {
+  const long long per = (D == 256 ? 1 : 2) * (ROWS / G);
+  const long long packed = (T + B * (per - 1)) / per, each = (max_len + per - 1) / per;
+  return (packed / B < each ? packed : each * B) * Hkv;
+}
+
+namespace {
 
 template <int D>
 cudaError_t plaunch(PromptArgs a, long long q_stride, const void* k, const void* v, long long kv_stride,
@@ -432,19 +655,21 @@ cudaError_t plaunch(PromptArgs a, long long q_stride, const void* k, const void*
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   auto kern = prompt_kernel<D>;
   if (!attr_set[dev]) {
+    if (C::MOVE_REGS) {                        // the shares fit what a launch gets
+      cudaFuncAttributes at;
+      const cudaError_t e = cudaFuncGetAttributes(&at, kern);
+      if (e != cudaSuccess) return e;
+      if (at.numRegs < C::REGS) return cudaErrorInvalidConfiguration;
+    }
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  const int per = C::NQ * (ROWS / G);
-  a.qtiles = (a.max_len + per - 1) / per;
-  kern<<<(unsigned)((long long)a.qtiles * a.B * a.Hkv), C::THREADS, C::SMEM, st>>>(a, qm, km, vm);
+  kern<<<(unsigned)prompt_items(D, G, a.T, a.max_len, a.B, a.Hkv), C::THREADS, C::SMEM, st>>>(a, qm, km, vm);
   return cudaGetLastError();
 }
 
 }  // namespace
-
-int prompt_positions_per_cta(int D, int G) { return (D == 256 ? 1 : 2) * (ROWS / G); }
 
 cudaError_t launch_prompt(int D, const PromptArgs& a, long long q_stride, const void* k, const void* v,
                           long long kv_stride, cudaStream_t st) {

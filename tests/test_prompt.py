@@ -22,7 +22,7 @@ def _call(**kw):
     ("INVALID_ARG", dict(start=None)), ("INVALID_ARG", dict(out=None)),
     ("INVALID_ARG", dict(qs=32 * 128 - 8)), ("INVALID_ARG", dict(ks=8 * 128 - 8)),
     ("INVALID_ARG", dict(qs=1 << 39)), ("INVALID_ARG", dict(ks=1 << 39)), ("INVALID_ARG", dict(qs=-8)),
-    ("INVALID_ARG", dict(B=(1 << 31) - 1)), ("INVALID_ARG", dict(B=1 << 20, most=1 << 30, T=1 << 30)),
+    ("INVALID_ARG", dict(B=(1 << 31) - 1)), ("INVALID_ARG", dict(B=1 << 30, most=1 << 20, T=(1 << 31) - 300)),
     ("ALIGNMENT", dict(qs=32 * 128 + 4)), ("ALIGNMENT", dict(ks=8 * 128 + 4)), ("ALIGNMENT", dict(q=OK + 8)),
     ("ALIGNMENT", dict(k=OK + 2)), ("ALIGNMENT", dict(v=OK + 4)), ("ALIGNMENT", dict(out=OK + 8)),
     ("ALIGNMENT", dict(start=OK + 2)),
