@@ -597,9 +597,9 @@ kvq_status kvq_prompt_attention(const kvq_ctx* ctx, int layer, const void* q,
  *   overlapping calls need one each.
  * Softmax and sums are fp32; over the prefix, the weight that meets a V code is
  * rounded as kvq_cross_attention says.  A layer with a window is
- * KVQ_ERR_UNSUPPORTED (it reads no long prefix).  A group with a negative start or
- * length, past the batch, or with a negative shared length sets KVQ_ERR_BAD_INDEX and
- * shares nothing; lengths and block ids as kvq_decode_attention treats them.  Scale
+ * KVQ_ERR_UNSUPPORTED (it reads no long prefix).  Starts that descend or leave
+ * [0, batch] set KVQ_ERR_BAD_INDEX and nothing is shared; a negative shared length sets
+ * it and its group shares nothing; lengths and block ids as kvq_decode_attention treats them.  Scale
  * pointers as for kvq_decode_attention. */
 kvq_status kvq_shared_prefix_attention(const kvq_ctx* ctx, int layer, const void* q,
                                        const void* k_cache, const void* v_cache,
@@ -611,10 +611,11 @@ kvq_status kvq_shared_prefix_attention(const kvq_ctx* ctx, int layer, const void
                                        int max_shared, int max_own, void* out, int num_splits,
                                        void* workspace, size_t workspace_bytes, void* stream);
 
-/* Splits of the prefixes and workspace bytes of a kvq_shared_prefix_attention call: on
- * input *num_splits > 0 (at most 1024) requests a count, 0 asks for the plan's choice;
- * on output it is 0 where nothing can be shared (no group of two rows, or no prefix of
- * 16 positions). */
+/* Splits of a prefix at most, and workspace bytes, of a kvq_shared_prefix_attention call:
+ * on input *num_splits > 0 (at most 1024) requests a bound, 0 asks for the plan's; on
+ * output it is 0 where nothing can be shared (no group of two rows, or no prefix of 16
+ * positions).  How the prefixes are cut within it is decided on the device, from their
+ * lengths. */
 kvq_status kvq_shared_prefix_plan(const kvq_ctx* ctx, int layer, int batch, int num_groups,
                                   int max_group, int max_shared, int max_own, int* num_splits,
                                   size_t* workspace_bytes);

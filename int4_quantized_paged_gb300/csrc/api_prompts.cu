@@ -86,13 +86,14 @@ int stream_once(const kvq_ctx* ctx, int layer, int batch, long long positions) {
 
 constexpr long long kMostWorkers = 4LL * 65535 * 64;
 
-// Sizes of a call behind shared prefixes: splits (0 in: the plan's choice), workers of
-// the rows' own positions, and the parts of the workspace.
+// Sizes of a call behind shared prefixes: splits of a prefix at most (0 in: the plan's
+// choice), workers of the rows' own positions, and the parts of the workspace.
 struct SharedPlan {
   int splits, workers;
+  int units, unit_rows;          // as in SharedArgs
   size_t rows;                   // partial rows of the prefixes
-  size_t index_bytes, prefix_bytes, own_bytes;
-  size_t bytes() const { return index_bytes + prefix_bytes + own_bytes; }
+  size_t index_bytes, unit_bytes, prefix_bytes, own_bytes;
+  size_t bytes() const { return index_bytes + unit_bytes + prefix_bytes + own_bytes; }
 };
 
 kvq_status plan_shared(const kvq_ctx* ctx, int layer, int batch, int num_groups, int max_group,
@@ -108,24 +109,29 @@ kvq_status plan_shared(const kvq_ctx* ctx, int layer, int batch, int num_groups,
   *p = {};
   if (num_groups > 0 && max_group > 1 && max_shared >= 16) {
     const int tile = cross_query_tile(c.head_dim, c.num_q_heads / c.num_kv_heads);
-    // CTAs of one split, in steps whose products fit 64 bits
-    long long base = ((long long)max_group + tile - 1) / tile * num_groups;
-    if (base >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
-    base *= c.num_kv_heads;
+    // units of one split, in steps whose products fit 64 bits
+    const long long base = ((long long)max_group + tile - 1) / tile * num_groups;
     if (base >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
     const int tiles = (int)(((long long)max_shared + CROSS_KEYS - 1) / CROSS_KEYS);
-    p->splits = num_splits > 0 ? num_splits : plan_splits(base, tiles);
-    if (base * p->splits >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
-    const long long rows = (long long)num_groups * max_group;      // below 2^62
-    if (rows >= (1LL << 34) / p->splits / c.num_q_heads) return KVQ_ERR_INVALID_ARG;
-    p->rows = (size_t)p->splits * (size_t)rows * c.num_q_heads;
+    // one wave over the SMs, or two units for each group where they are more than that
+    const long long wave = (sm_count() + c.num_kv_heads - 1) / c.num_kv_heads;
+    p->splits = num_splits > 0 ? num_splits : (int)(tiles < wave ? tiles : wave);
+    long long units = base * p->splits;
+    const long long most = 2 * base > wave ? 2 * base : wave;
+    if (units > most) units = most;
+    if (units >= (1LL << 31) / c.num_kv_heads) return KVQ_ERR_INVALID_ARG;
+    p->units = (int)units;
+    p->unit_rows = max_group < tile ? max_group : tile;
+    if (units >= (1LL << 34) / p->unit_rows / c.num_q_heads) return KVQ_ERR_INVALID_ARG;
+    p->rows = (size_t)units * p->unit_rows * c.num_q_heads;
   }
   // a prefix is cut to whole tiles of 16, and what is left over is a row's own
   int workers = 0;
   st = kvq_decode_plan(ctx, layer, batch, max_own + 15, &workers, nullptr);
   if (st != KVQ_OK) return st;
   p->workers = workers;
-  p->index_bytes = align16(((size_t)batch * 2 + (size_t)num_groups) * sizeof(int));
+  p->index_bytes = align16(((size_t)batch * 2 + (size_t)num_groups * 3 + 1) * sizeof(int));
+  p->unit_bytes = (size_t)p->units * sizeof(int4);
   p->prefix_bytes = align16(p->rows * (c.head_dim + 1) * sizeof(float));
   p->own_bytes = partial_bytes(c, batch, workers);
   return KVQ_OK;
@@ -216,7 +222,7 @@ kvq_status kvq_shared_prefix_attention(const kvq_ctx* ctx, int layer, const void
   if ((long long)max_blocks_per_seq * c.block_size >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
   if (num_groups > 0 && (!group_start || !shared_lens)) return KVQ_ERR_INVALID_ARG;
   if (!aligned4(group_start) || !aligned4(shared_lens)) return KVQ_ERR_ALIGNMENT;
-  if ((long long)batch * c.num_q_heads >= (1LL << 31) || p.workers > kMostWorkers)
+  if ((long long)batch * c.num_kv_heads >= (1LL << 31) || p.workers > kMostWorkers)
     return KVQ_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < p.bytes()) return KVQ_ERR_WORKSPACE;
   if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
@@ -230,16 +236,22 @@ kvq_status kvq_shared_prefix_attention(const kvq_ctx* ctx, int layer, const void
   x.shared_lens = shared_lens;
   x.groups = num_groups;
   x.max_group = max_group < batch ? max_group : batch;
-  x.splits = p.splits;
-  const int tiles = (max_shared + CROSS_KEYS - 1) / CROSS_KEYS;
-  x.split_tiles = p.splits > 0 ? (tiles + p.splits - 1) / p.splits : 1;
-  x.first = reinterpret_cast<int*>(ws);
+  x.max_splits = p.splits;
+  x.max_units = p.units;
+  x.unit_rows = p.unit_rows;
+  x.tile = cross_query_tile(c.head_dim, c.num_q_heads / c.num_kv_heads);
+  x.sms = sm_count();
+  // index: (first unit, splits) of each group, which want 8-byte alignment, lead
+  x.at = reinterpret_cast<int2*>(ws);
+  x.first = reinterpret_cast<int*>(x.at + num_groups);
   x.group_of = x.first + batch;
   x.prefix = x.group_of + batch;
-  x.o = reinterpret_cast<float*>(ws + p.index_bytes);
+  x.num_units = x.prefix + num_groups;
+  x.units = reinterpret_cast<int4*>(ws + p.index_bytes);
+  x.o = reinterpret_cast<float*>(ws + p.index_bytes + p.unit_bytes);
   x.lse = x.o + p.rows * c.head_dim;
   a.first = x.first;
-  place_partials(c, &a, ws + p.index_bytes + p.prefix_bytes);
+  place_partials(c, &a, ws + p.index_bytes + p.unit_bytes + p.prefix_bytes);
   return cuda_status(launch_shared(ctx->mode[layer], c.head_dim, c.num_q_heads / c.num_kv_heads, a,
                                    x, static_cast<cudaStream_t>(stream)));
 }

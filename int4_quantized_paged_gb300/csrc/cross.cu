@@ -176,10 +176,10 @@ cudaError_t claunch(const PrefillArgs& pa, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  const long long grid = (long long)pa.qtiles * pa.splits * a.B * a.Hkv;
+  const long long grid = pa.units ? (long long)pa.splits * a.Hkv : (long long)pa.qtiles * pa.splits * a.B * a.Hkv;
   kern<<<(unsigned)grid, WRoles<MODE, D, FEW>::THREADS, C::SMEM, st>>>(pa, km, vm);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || pa.splits <= 1 || pa.shared) return e;
+  if (e != cudaSuccess || pa.splits <= 1 || pa.units) return e;
   const long long items = (long long)a.B * pa.max_query * a.Hq;
   // its launch overlaps the attention's tail
   const int wpr = pa.splits <= 8 ? 1 : (pa.splits <= 16 ? 2 : (pa.splits <= 32 ? 4 : 8));
@@ -218,18 +218,7 @@ int cross_query_tile(int D, int G) {
 
 namespace {
 
-cudaError_t launch(int mode, int D, int G, const DecodeArgs& a, const int* query_start,
-                   int max_query_len, int splits, int split_tiles, int shared, cudaStream_t st) {
-  PrefillArgs pa = {};
-  pa.shared = shared;
-  pa.d = a;
-  pa.query_start = query_start;
-  const int tile = cross_query_tile(D, G);
-  pa.qtiles = (max_query_len + tile - 1) / tile;
-  pa.g_shift = __builtin_ctz((unsigned)G);
-  pa.max_query = max_query_len;
-  pa.splits = splits;
-  pa.split_tiles = split_tiles;
+cudaError_t launch(int mode, int D, int G, const PrefillArgs& pa, cudaStream_t st) {
   switch (mode) {
     case BF16: return claunch_d<BF16>(D, pa, st);
     case FP8_PER_TENSOR: return claunch_d<FP8_PER_TENSOR>(D, pa, st);
@@ -244,12 +233,30 @@ cudaError_t launch(int mode, int D, int G, const DecodeArgs& a, const int* query
 
 cudaError_t launch_cross(int mode, int D, int G, const DecodeArgs& a, const int* query_start,
                          int max_query_len, int splits, int split_tiles, cudaStream_t st) {
-  return launch(mode, D, G, a, query_start, max_query_len, splits, split_tiles, 0, st);
+  PrefillArgs pa = {};
+  pa.d = a;
+  pa.query_start = query_start;
+  const int tile = cross_query_tile(D, G);
+  pa.qtiles = (max_query_len + tile - 1) / tile;
+  pa.g_shift = __builtin_ctz((unsigned)G);
+  pa.max_query = max_query_len;
+  pa.splits = splits;
+  pa.split_tiles = split_tiles;
+  return launch(mode, D, G, pa, st);
 }
 
-cudaError_t launch_prefix(int mode, int D, int G, const DecodeArgs& a, const int* group_start,
-                          int max_group, int splits, int split_tiles, cudaStream_t st) {
-  return launch(mode, D, G, a, group_start, max_group, splits, split_tiles, 1, st);
+cudaError_t launch_prefix(int mode, int D, int G, const DecodeArgs& a, const SharedArgs& x, cudaStream_t st) {
+  PrefillArgs pa = {};
+  pa.d = a;
+  pa.query_start = x.group_start;
+  pa.qtiles = 1;                               // not read: a unit names its query tile
+  pa.g_shift = __builtin_ctz((unsigned)G);
+  pa.max_query = x.max_group;
+  pa.splits = x.max_units;                     // CTAs per KV head
+  pa.units = x.units;
+  pa.num_units = x.num_units;
+  pa.unit_rows = x.unit_rows;
+  return launch(mode, D, G, pa, st);
 }
 
 }  // namespace kvq

@@ -278,11 +278,10 @@ struct Layout {
 };
 
 // What a launch computes:
-//  DECODE_PLAIN    the attention output;
-//  DECODE_WEIGHTS  that, and the scores (log2 units) of every position read and the
-//                  log2 of each row's weight sum, from which the weights follow;
-//  DECODE_OWN      partials of the positions from first[b] on, never an output (what
-//                  lies before them is another kernel's, and both are joined).
+//  DECODE_PLAIN    the attention output, or partials that merge_kernel joins;
+//  DECODE_WEIGHTS  partials, and the scores (log2 units) of every position read;
+//  DECODE_OWN      partials of the positions from first[b] on (what lies before them is
+//                  another kernel's).
 enum Kind { DECODE_PLAIN, DECODE_WEIGHTS, DECODE_OWN };
 
 // Position of one warp's cursor in the tile list.
@@ -440,7 +439,7 @@ __device__ void publish_items(const DecodeArgs& a, int lane) {
       const long long first = base + incl - (long long)n * a.Hkv;
       if (a.item_tiles)
         for (int g = 0; g < a.Hkv; ++g) a.item_tiles[(long long)b * a.Hkv + g] = first + (long long)g * n;
-      if (KIND != DECODE_OWN && n == 0) {
+      if (KIND == DECODE_PLAIN && n == 0) {
         if (a.out_bf16) {
           uint4* o = reinterpret_cast<uint4*>(a.out_bf16 + (long long)b * a.Hq * D);
           for (int i = 0; i < a.Hq * D / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -634,7 +633,7 @@ __global__ void __launch_bounds__(WARPS * 32, MinCtas<MODE, D, G>::value)
     else unscale = vsg * (1.f / PSTATIC);
     const int nh = (G == 1) ? 1 : 2;              // heads owned by this lane column
     const bool owner = (G == 1) ? (lt == 0) : (2 * lt < G);
-    const bool full = KIND != DECODE_OWN && seg_k0 == 0 && seg_klast == seg_n - 1;
+    const bool full = KIND == DECODE_PLAIN && seg_k0 == 0 && seg_klast == seg_n - 1;
     const int item = seg_b * a.Hkv + seg_g;
     if (owner) {
 #pragma unroll
@@ -661,8 +660,6 @@ __global__ void __launch_bounds__(WARPS * 32, MinCtas<MODE, D, G>::value)
             *reinterpret_cast<float2*>(dst + d) = make_float2(o[i][e1] * f, o[i][2 + e1] * f_odd);
           }
         }
-        if constexpr (KIND == DECODE_WEIGHTS)
-          if (full && lg == 0) a.lse[(long long)seg_b * a.Hq + seg_g * G + h] = m_run[e1] + log2f(l);
         if (!full && lg == 0) {
           float* ml = a.ws_ml + 2 * ((long long)(item + wid) * G + h);
           ml[0] = m_run[e1];
@@ -978,7 +975,7 @@ __global__ void __launch_bounds__(WARPS * 32, MinCtas<MODE, D, G>::value)
 // partial rows of the first PRE workers are loaded together with the (m, l)
 // pairs, so an item split over at most PRE workers costs two dependent rounds
 // of loads after the item offsets.
-template <int D, int G, int KIND = DECODE_PLAIN>
+template <int D, int G>
 __global__ void __launch_bounds__(32 * G) merge_kernel(const DecodeArgs a) {
   // launched as a programmatic dependent of the decode kernel: wait until that
   // grid has completed and its writes are visible
@@ -1065,8 +1062,6 @@ __global__ void __launch_bounds__(32 * G) merge_kernel(const DecodeArgs a) {
   }
   const long long orow = ((long long)b * a.Hq + g * G + j) * D;
   const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
-  if constexpr (KIND == DECODE_WEIGHTS)
-    if (lane == 0) a.lse[(long long)b * a.Hq + g * G + j] = M + log2f(lsum);
   if (a.out_bf16) {
 #pragma unroll
     for (int k = 0; k < DL; ++k)

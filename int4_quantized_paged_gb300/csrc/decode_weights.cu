@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include "decode_kernel.cuh"
+#include "join.cuh"
 
 namespace kvq {
 namespace {
@@ -92,10 +93,8 @@ struct WeightsOp {
     decode_kernel<MODE, D, G, DECODE_WEIGHTS><<<ctas, WARPS * 32, smem, st>>>(a, km, vm);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (a.workers > 1) {
-      e = launch_dependent(merge_kernel<D, G, DECODE_WEIGHTS>, dim3((unsigned)(a.B * a.Hkv)), 32 * G, 0, st, a);
-      if (e != cudaSuccess) return e;
-    }
+    e = launch_dependent(join_kernel<D, G, false>, dim3((unsigned)(a.B * a.Hkv)), JT, 0, st, a, SharedArgs{});
+    if (e != cudaSuccess) return e;
     const unsigned parts = (unsigned)((a.cap + AT * AU - 1) / (AT * AU));
     if (parts == 0) return cudaSuccess;
     return launch_dependent(accumulate_kernel<G>, dim3(parts, (unsigned)a.Hkv, (unsigned)a.B), AT, 0, st, a,

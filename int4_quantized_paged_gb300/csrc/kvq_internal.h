@@ -149,17 +149,24 @@ struct EvictArgs {
   int seg_max;                 // set by the launcher: cells of a CTA at most
 };
 
-// Decode behind shared prefixes (beside DecodeArgs).
+// Decode behind shared prefixes (beside DecodeArgs).  A unit is a split of a group's
+// prefix against a query tile of its rows, for every KV head.
 struct SharedArgs {
   const int* group_start;      // [groups + 1] rows of each group
   const int* shared_lens;      // [groups]
   int groups, max_group;
-  int splits, split_tiles;     // of the prefixes, as for the cross attention
+  int max_splits;              // of one prefix
+  int max_units, unit_rows;    // units, and rows of each, that there is room for
+  int tile;                    // rows of a query tile
+  int sms;
   int* first;                  // [B] where a row's own positions begin
   int* group_of;               // [B] its group, -1: nothing shared
   int* prefix;                 // [groups] positions that the group shares
-  float* o;                    // [splits][groups][max_group][Hq][D]
-  float* lse;                  // [splits][groups][max_group][Hq]
+  int2* at;                    // [groups] its first unit, its splits
+  int4* units;                 // [max_units] (group, split, query tile, key tiles per split)
+  int* num_units;
+  float* o;                    // [max_units][unit_rows][Hq][D]
+  float* lse;                  // [max_units][unit_rows][Hq]
 };
 
 // Launchers (return cudaGetLastError() of the launch).
@@ -222,10 +229,9 @@ cudaError_t launch_prompt(int D, const PromptArgs& a, long long q_stride, const 
 int evict_cluster(int max_len, long long items);
 cudaError_t launch_evict(EvictArgs a, int n, cudaStream_t st);
 
-// The cross attention's kernel with partial results only: the groups' rows against
-// the first prefix positions of their first row (context_lens: the prefixes).
-cudaError_t launch_prefix(int mode, int D, int G, const DecodeArgs& a, const int* group_start,
-                          int max_group, int splits, int split_tiles, cudaStream_t st);
+// The cross attention's kernel over the units of *x: partial results only.
+cudaError_t launch_prefix(int mode, int D, int G, const DecodeArgs& a, const SharedArgs& x,
+                          cudaStream_t st);
 cudaError_t launch_shared(int mode, int D, int G, const DecodeArgs& a, const SharedArgs& x,
                           cudaStream_t st);
 cudaError_t launch_decode_weights(int mode, int D, int G, const DecodeArgs& a, float* weights,

@@ -18,9 +18,12 @@ struct PrefillArgs {
   int max_query;                 // the caller's bound of a sequence's queries
   int splits;                    // splits of a sequence's keys, at most
   int split_tiles;               // key tiles (of 64) per split; the last takes what is left
-  // the sequences are groups of rows that share a prefix: the pages are those of the
-  // group's first row, and every split leaves a partial
-  int shared;
+  // The sequences are groups of rows that share a prefix (nullptr: they are not): the
+  // pages are those of a group's first row, CTA (unit, KV head) takes units[unit] =
+  // (group, split, query tile, key tiles per split), and leaves a partial there.
+  const int4* units;
+  const int* num_units;
+  int unit_rows;                 // queries of a unit's partial
 };
 
 // 16 raw code bytes -> their f16 (bf16 for BF16) values: 8 (BF16), 16 (FP8)

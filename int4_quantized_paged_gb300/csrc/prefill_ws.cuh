@@ -233,15 +233,27 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
   // CROSS: the query tiles of one (split, sequence, KV head) are neighbours, so
   // that they read its pages from L2.
   const int per_tile = a.B * a.Hkv;
-  const int ct = CROSS ? (int)(blockIdx.x % pa.qtiles) : pa.qtiles - 1 - (int)(blockIdx.x / per_tile);
+  int ct = CROSS ? (int)(blockIdx.x % pa.qtiles) : pa.qtiles - 1 - (int)(blockIdx.x / per_tile);
   const int rem = CROSS ? (int)(blockIdx.x / pa.qtiles) % per_tile : (int)(blockIdx.x % per_tile);
-  const int split = CROSS ? (int)(blockIdx.x / pa.qtiles) / per_tile : 0;
-  const int b = rem / a.Hkv, g = rem - b * a.Hkv;
+  int split = CROSS ? (int)(blockIdx.x / pa.qtiles) / per_tile : 0;
+  int b = rem / a.Hkv, g = rem - b * a.Hkv;
+  int split_tiles = CROSS ? pa.split_tiles : 0, unit = 0;
+  if constexpr (CROSS) {
+    if (pa.units) {                                         // of prefixes that groups share
+      unit = blockIdx.x / a.Hkv;
+      if (unit >= *pa.num_units) return;
+      const int4 u = pa.units[unit];
+      b = u.x;
+      g = blockIdx.x - unit * a.Hkv;
+      split = u.y;
+      ct = u.z;
+      split_tiles = u.w;
+    }
+  }
   const int q0 = pa.query_start[b];
   int n_b = pa.query_start[b + 1] - q0;
   const int L = a.context_lens[b];
   if constexpr (CROSS) {
-    if (pa.shared && L <= 0) return;                        // nothing shared: its rows are others' work
     if (n_b > pa.max_query) {                               // rows past the caller's bound
       if (tid == 0) atomicOr(a.err, ERR_BAD_INDEX);
       n_b = pa.max_query;
@@ -275,12 +287,12 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
         }
       return;
     }
-    const int ts = split * pa.split_tiles;
+    const int ts = split * split_tiles;
     if (ts >= tiles) return;
-    const bool last = split == pa.splits - 1;
-    whole = !pa.shared && (pa.splits <= 1 || tiles <= pa.split_tiles);
+    const bool last = !pa.units && split == pa.splits - 1;
+    whole = !pa.units && (pa.splits <= 1 || tiles <= split_tiles);
     kmin = ts * WKT;
-    pmax = (last ? L : min(L, (ts + pa.split_tiles) * WKT)) - 1;
+    pmax = (last ? L : min(L, (ts + split_tiles) * WKT)) - 1;
     first = pmax;                                           // every row sees the same keys
   } else {
     first = L - n_b + qbase;
@@ -486,7 +498,7 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
         const int pt = 32 * c + lane;
         const int pos = t0 * WKT + 16 * pt;
         if (pt >= SUB * ntl || pos + 16 <= kmin || pos > pmax) return -1;
-        const int row = CROSS && pa.shared ? q0 : b;
+        const int row = CROSS && pa.units ? q0 : b;
         const int blk = __ldg(a.block_table + (long long)row * a.max_blocks + (pos >> a.bs_shift));
         if (blk >= 0 && blk < a.num_blocks) return blk;
         atomicOr(a.err, ERR_BAD_INDEX);
@@ -1058,8 +1070,9 @@ __global__ void __launch_bounds__(WRoles<MODE, D, FEW>::THREADS, 1)
       if constexpr (CROSS) {
         const int qi = qbase + j * QP + ii;
         const long long orow = (long long)(q0 + qi) * a.Hq + g * heads + h;
-        const long long prow = (((long long)split * a.B + b) * pa.max_query + qi) * a.Hq +
-                               g * heads + h;
+        const long long part = pa.units ? (long long)unit * pa.unit_rows + (qi - qbase)
+                                        : ((long long)split * a.B + b) * pa.max_query + qi;
+        const long long prow = part * a.Hq + g * heads + h;
         // weight of this row's O, and of its copies'
         float w0 = f, wc[4] = {0.f, 0.f, 0.f, 0.f};
         const int copies = FEW ? 1 << copies_shift : 1;

@@ -9,9 +9,13 @@
 //
 // Structure.  Four launches:
 //  * plan_kernel, one CTA: each group's prefix as it can be shared (cut to its
-//    shortest row and to whole tiles of 16), and for each row where its own begins;
-//  * the warp-specialised attention of cross.cu, the groups as its sequences: rows x
-//    heads on the tensor cores, the prefix cut into splits that fill the SMs;
+//    shortest row and to whole tiles of 16), for each row where its own begins, and the
+//    units of work: the prefixes cut into splits of as many key tiles as take the
+//    least time over the SMs.  The host does not know the lengths, and splits of equal
+//    numbers left most SMs waiting for the longest prefix (six groups of 100-8,000
+//    positions, 1-30 rows: 52 us; cut by the lengths 35);
+//  * the warp-specialised attention of cross.cu over the units: rows x heads on the
+//    tensor cores;
 //  * the decode kernel over the rows' own positions, which begins while the prefixes'
 //    last CTAs run (it does not read their results);
 //  * join_kernel: all partials of a row.
@@ -22,6 +26,7 @@
 #include <cuda_runtime.h>
 
 #include "decode_kernel.cuh"
+#include "join.cuh"
 
 namespace kvq {
 namespace {
@@ -30,148 +35,102 @@ constexpr int PT = 1024;
 constexpr int MIN_ROWS = 2;                    // rows of a group that are worth a shared pass
 
 __global__ void __launch_bounds__(PT) plan_kernel(const DecodeArgs a, const SharedArgs x) {
+  __shared__ unsigned long long s_best;
+  __shared__ int s_most;
   for (int b = threadIdx.x; b < a.B; b += PT) {
     x.first[b] = 0;
     x.group_of[b] = -1;
   }
-  __syncthreads();
+  if (threadIdx.x == 0) {
+    s_best = ~0ull;
+    s_most = 0;
+  }
+  // starts that do not ascend within the batch might put a row into two groups
+  bool astray = false;
+  for (int g = threadIdx.x; g < x.groups; g += PT) {
+    const int r0 = x.group_start[g], r1 = x.group_start[g + 1];
+    astray |= r0 < 0 || r1 < r0 || r1 > a.B;
+  }
+  astray = __syncthreads_or(astray);
+  if (astray && threadIdx.x == 0) atomicOr(a.err, ERR_BAD_INDEX);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int g = warp; g < x.groups; g += PT / 32) {
     const int r0 = x.group_start[g], r1 = x.group_start[g + 1], P = x.shared_lens[g];
-    const bool bad = r0 < 0 || r1 < r0 || r1 > a.B || P < 0;
-    if (bad && lane == 0) atomicOr(a.err, ERR_BAD_INDEX);
+    if (P < 0 && lane == 0) atomicOr(a.err, ERR_BAD_INDEX);
     int shared = 0;
     // rows past the caller's bound, and a row by itself, read their prefix alone
-    if (!bad && r1 - r0 >= MIN_ROWS && r1 - r0 <= x.max_group) {
+    if (!astray && P > 0 && x.max_units > 0 && r1 - r0 >= MIN_ROWS && r1 - r0 <= x.max_group) {
       shared = P;
       for (int b = r0 + lane; b < r1; b += 32) shared = min(shared, ctx_len(a, b));
       shared = __reduce_min_sync(0xffffffffu, shared) & ~(TILE - 1);
     }
-    if (lane == 0) x.prefix[g] = shared;
+    if (lane == 0) {
+      x.prefix[g] = shared;
+      atomicMax(&s_most, (shared + CROSS_KEYS - 1) / CROSS_KEYS);
+    }
     if (shared > 0)
       for (int b = r0 + lane; b < r1; b += 32) {
         x.first[b] = shared;
         x.group_of[b] = g;
       }
   }
-}
-
-// One CTA per (row, query head): JW warps take its partials in turn, and meet in
-// shared memory.
-constexpr int JW = 4;
-
-template <int D>
-__global__ void __launch_bounds__(JW * 32) join_kernel(const DecodeArgs a, const SharedArgs x) {
-  constexpr int DL = D / 64;                   // float2 pairs per lane
-  __shared__ float2 s_o[JW][DL][32];
-  __shared__ float s_top[JW], s_sum[JW];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq;
-  const int G = a.Hq / a.Hkv, kvh = h / G, j = h - kvh * G;
-  // launched as a programmatic dependent: all partials are visible below
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the prefix's splits: O / l, and the log2 of the weights' sum
-  const int grp = x.group_of[b];
-  int ns = 0;
-  long long p0 = 0;
-  if (grp >= 0) {
-    const int tiles = (x.prefix[grp] + CROSS_KEYS - 1) / CROSS_KEYS;
-    ns = min(x.splits, (tiles + x.split_tiles - 1) / x.split_tiles);
-    p0 = ((long long)grp * x.max_group + (b - x.group_start[grp])) * a.Hq + h;
-  }
-  const long long step = (long long)x.groups * x.max_group * a.Hq;
-  // the workers of the row's own positions: O, running maximum and sum
-  const int item = b * a.Hkv + kvh;
-  long long w0 = 0, nw = 0;
-  const long long W = a.workers, T = a.item_tiles[(long long)a.B * a.Hkv];
-  {
-    const long long first = a.item_tiles[item], n = a.item_tiles[item + 1] - first;
-    if (n > 0) {
-      w0 = ((first + 1) * W - 1) / T;
-      nw = ((first + n) * W - 1) / T - w0 + 1;
-    }
-  }
-  float top = -INFINITY, sum = 0.f;
-  float2 acc[DL];
-#pragma unroll
-  for (int k = 0; k < DL; ++k) acc[k] = make_float2(0.f, 0.f);
-  // parts 0 .. ns - 1 are splits, the others workers; four in flight a warp
-  for (long long s0 = warp; s0 < ns + nw; s0 += 4 * JW) {
-    float e[4], f[4];                          // log2 of a part's weight, and its sum over it
-    float2 v[4][DL];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const long long s = s0 + u * JW;
-      e[u] = -INFINITY;
-      f[u] = 0.f;
-#pragma unroll
-      for (int k = 0; k < DL; ++k) v[u][k] = make_float2(0.f, 0.f);
-      const float* o = nullptr;
-      if (s < ns) {
-        const long long p = p0 + s * step;
-        e[u] = x.lse[p];
-        f[u] = 1.f;
-        o = x.o + p * D;
-      } else if (s < ns + nw) {
-        const long long w = w0 + (s - ns);
-        // a worker whose share is empty wrote nothing
-        if ((w * T) / W != ((w + 1) * T) / W) {
-          const long long part = (item + w) * G + j;
-          e[u] = a.ws_ml[2 * part];
-          f[u] = a.ws_ml[2 * part + 1];
-          o = a.ws_o + part * D;
-        }
-      }
-      if (o && e[u] != -INFINITY) {
-#pragma unroll
-        for (int k = 0; k < DL; ++k) v[u][k] = reinterpret_cast<const float2*>(o)[lane + 32 * k];
-      }
-    }
-    float m = top;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) m = fmaxf(m, e[u]);
-    const float ref = m == -INFINITY ? 0.f : m;
-    const float old = ex2(top - ref);
-    sum *= old;
-#pragma unroll
-    for (int k = 0; k < DL; ++k) { acc[k].x *= old; acc[k].y *= old; }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float w = ex2(e[u] - ref);
-      sum = fmaf(w, f[u], sum);
-#pragma unroll
-      for (int k = 0; k < DL; ++k) {
-        acc[k].x = fmaf(w, v[u][k].x, acc[k].x);
-        acc[k].y = fmaf(w, v[u][k].y, acc[k].y);
-      }
-    }
-    top = m;
-  }
-#pragma unroll
-  for (int k = 0; k < DL; ++k) s_o[warp][k][lane] = acc[k];
-  if (lane == 0) { s_top[warp] = top; s_sum[warp] = sum; }
   __syncthreads();
-  float m = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < JW; ++w) m = fmaxf(m, s_top[w]);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float f[JW], all = 0.f;
-#pragma unroll
-  for (int w = 0; w < JW; ++w) {
-    f[w] = ex2(s_top[w] - ref);
-    all = fmaf(f[w], s_sum[w], all);
+  const int most = s_most;
+  if (most == 0) {                             // nothing is shared
+    if (threadIdx.x == 0) *x.num_units = 0;
+    return;
   }
-  const float inv = all > 0.f ? 1.f / all : 0.f;   // a row without positions: zeros
-  uint32_t* out = reinterpret_cast<uint32_t*>(a.out_bf16 + ((long long)b * a.Hq + h) * D);
-  for (int k = warp; k < DL; k += JW) {
-    float2 r = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < JW; ++w) {
-      const float2 v = s_o[w][k][lane];
-      r.x = fmaf(f[w], v.x, r.x);
-      r.y = fmaf(f[w], v.y, r.y);
+  // Query tiles and key tiles of a group (its rows were checked above).
+  auto sizes = [&](int g, int* tiles) {
+    *tiles = (x.prefix[g] + CROSS_KEYS - 1) / CROSS_KEYS;
+    return *tiles > 0 ? (x.group_start[g + 1] - x.group_start[g] + x.tile - 1) / x.tile : 0;
+  };
+  // Key tiles per split: a CTA costs its tiles and about three more, and CTAs come in
+  // waves over the SMs.  Each thread prices its own counts; of equal ones the larger
+  // splits win.
+  const int least = (most + x.max_splits - 1) / x.max_splits;
+  for (int t = least + threadIdx.x; t <= most; t += PT) {
+    long long units = 0;
+    for (int g = 0; g < x.groups; ++g) {
+      int tiles;
+      const int q = sizes(g, &tiles);
+      units += (long long)q * ((tiles + t - 1) / t);
     }
-    out[lane + 32 * k] = pack_bf16x2(r.x * inv, r.y * inv);
+    if (units > x.max_units && t < most) continue;
+    const unsigned long long waves = (unsigned long long)((units * a.Hkv + x.sms - 1) / x.sms);
+    atomicMin(&s_best, (waves * (unsigned)(t + 3)) << 31 | (unsigned)(0x7fffffff - t));
+  }
+  __syncthreads();
+  const int per = 0x7fffffff - (int)(s_best & 0x7fffffffu);
+  // The list of units: a group's query tiles are neighbours, so that they read its pages
+  // from L2.
+  if (warp == 0) {
+    int base = 0;
+    for (int g0 = 0; g0 < x.groups; g0 += 32) {
+      const int g = g0 + lane;
+      int tiles = 0, q = 0, splits = 0;
+      if (g < x.groups) {
+        q = sizes(g, &tiles);
+        splits = (tiles + per - 1) / per;
+      }
+      int incl = q * splits;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const int first = base + incl - q * splits;
+      if (g < x.groups) x.at[g] = make_int2(first, splits);
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) *x.num_units = base;
+  }
+  __syncthreads();
+  for (int g = warp; g < x.groups; g += PT / 32) {
+    int tiles;
+    const int q = sizes(g, &tiles);
+    const int2 at = x.at[g];
+    for (int i = lane; i < q * at.y; i += 32) x.units[at.x + i] = make_int4(g, i / q, i % q, per);
   }
 }
 
@@ -202,7 +161,7 @@ struct OwnOp {
       e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
-    return launch_dependent(join_kernel<D>, dim3((unsigned)((long long)a.B * a.Hq)), JW * 32, 0, st, a, x);
+    return launch_dependent(join_kernel<D, G, true>, dim3((unsigned)(a.B * a.Hkv)), JT, 0, st, a, x);
   }
 };
 
@@ -212,14 +171,14 @@ cudaError_t launch_shared(int mode, int D, int G, const DecodeArgs& a, const Sha
   plan_kernel<<<1, PT, 0, st>>>(a, x);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const bool prefix = x.groups > 0 && x.max_group >= MIN_ROWS && x.splits > 0;
+  const bool prefix = x.max_units > 0;
   if (prefix) {
     DecodeArgs p = a;
     p.B = x.groups;
     p.context_lens = x.prefix;
     p.ws_o = x.o;
     p.ws_ml = x.lse;
-    e = launch_prefix(mode, D, G, p, x.group_start, x.max_group, x.splits, x.split_tiles, st);
+    e = launch_prefix(mode, D, G, p, x, st);
     if (e != cudaSuccess) return e;
   }
   return with_layer(mode, D, G, OwnOp{a, x, prefix, st});

@@ -168,6 +168,16 @@ def test_bad_groups_share_nothing():
         c.check(BAD)
 
 
+def test_many_groups():
+    """More groups than SMs, of all lengths; and one long prefix among short ones."""
+    c = Case(3, 64, 4, 2, [(1 + (37 * i) % 300, [1 + i % 5, 2]) for i in range(170)], seed=20)
+    c.run()
+    c.check()
+    c = Case(1, 128, 8, 2, [(40, [1, 2]), (9000, [3, 1, 1]), (70, [5, 5]), (1, [2, 2])], seed=21)
+    c.run()
+    c.check()
+
+
 def test_lengths_and_blocks_out_of_range():
     c = Case(1, 128, 8, 2, [(100, [5, 7, 9])], lone=[60], seed=11)
     c.T[3, 1] = c.blocks                          # that page's positions are left out

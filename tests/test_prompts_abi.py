@@ -20,8 +20,8 @@ def _plan(ctx=None, layer=0, batch=16, groups=2, splits=0, **kw):
 def test_shared_plan():
     splits, need = _plan()
     assert splits >= 1 and need % 16 == 0
-    partial = 2 * 8 * 32 * 129 * 4
-    assert _plan(splits=7)[1] - _plan(splits=5)[1] == 2 * partial
+    # two groups, a unit for each split: its entry, and a partial of 8 rows
+    assert _plan(splits=7)[1] - _plan(splits=5)[1] == 2 * 2 * (16 + 8 * 32 * 129 * 4)
     assert _plan(splits=7)[0] == 7
     # nothing to share: no splits and no room for them
     for kw in (dict(groups=0), dict(max_group=1), dict(max_shared=15), dict(batch=1)):
@@ -37,7 +37,7 @@ def test_shared_plan():
     ("INVALID_ARG", dict(splits=-1)), ("INVALID_ARG", dict(splits=1025)),
     ("INVALID_ARG", dict(groups=(1 << 31) - 1, batch=(1 << 31) - 1, max_group=(1 << 31) - 1)),
     ("INVALID_ARG", dict(groups=1 << 20, batch=1 << 20, max_group=1 << 20)),
-    ("INVALID_ARG", dict(groups=1 << 24, batch=1 << 24, max_group=8, splits=1024)),
+    ("INVALID_ARG", dict(groups=1 << 26, batch=1 << 27, max_group=8, splits=1024)),
     ("UNSUPPORTED", dict(ctx=_ctx((3,), [128]))),
 ])
 def test_shared_plan_refuses(match, kw):
