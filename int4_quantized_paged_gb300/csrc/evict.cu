@@ -32,10 +32,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int ET = 256;                        // threads per CTA, one per histogram bin
+constexpr int ET = 256;                        // threads per CTA, one per bin
 constexpr int EW = ET / 32;
+constexpr int BINS = 256;
+static_assert(BINS == ET, "a thread per bin");
 constexpr int MAX_CLUSTER = 8;
 constexpr int MAX_SEGMENT = 48 * 1024;         // cells of a CTA (their weights: 192 KB)
+static_assert(MAX_SEGMENT < 65536, "two counts of cells in 32 bits");
 constexpr int MOVE_U = 8;                      // 16-byte chunks in flight per thread
 
 // The weight's bits in an order that unsigned integers have; NaN lowest, -0 as 0.
@@ -75,7 +78,7 @@ __device__ __forceinline__ uint32_t range_bits(int p, int lo, int hi) {
   return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
-__global__ void __launch_bounds__(ET) evict_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(ET, 3) evict_kernel(const EvictArgs a) {
   cg::cluster_group cl = cg::this_cluster();
   const int cs = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -86,11 +89,17 @@ __global__ void __launch_bounds__(ET) evict_kernel(const EvictArgs a) {
   extern __shared__ uint32_t dyn[];
   uint32_t* keys = dyn;                        // [seg]; later the lists of moves
   uint32_t* s_gt = dyn + a.seg_max;            // [seg / 32] above the threshold, then: stays
-  uint32_t* s_eq = s_gt + a.seg_max / 32;      // [seg / 32] at the threshold
-  __shared__ int hist[2][ET];
+  uint32_t* s_eq = s_gt + a.seg_max / 32;      // [seg / 32] at the threshold, then: counts before
+  __shared__ int hist[BINS];                   // this CTA's, of one pass
+  __shared__ int sums[4][BINS];                // the cluster's, a row per pass
   __shared__ int s_warp[EW];
-  __shared__ int s_pick[3];                    // bin, weights of it still wanted, weights in it
   __shared__ int s_bad, s_count[3];            // what the other CTAs read: ties, places, survivors
+
+  // A CTA by itself needs no barrier of a cluster, which takes ten times as long.
+  auto sync_all = [&] {
+    if (cs > 1) cl.sync();
+    else __syncthreads();
+  };
 
   // ---- the row (every CTA of its heads comes to the same result)
   const int row = a.rows[i], keep = a.keep_lens[i];
@@ -117,9 +126,26 @@ __global__ void __launch_bounds__(ET) evict_kernel(const EvictArgs a) {
   const int c0 = min(max(lo - base, 0), seg), c1 = min(max(hi - base, 0), seg);
   const int wanted = keep - a.first - a.last;
 
+  // The sum of one int over the cluster's CTAs, and over those before this one.  All
+  // loads are under way at once: a remote one takes about as long as one to L2.
+  auto sum_of = [&](int* mine, int* before) -> int {
+    int v[MAX_CLUSTER], all = 0, low = 0;
+#pragma unroll
+    for (int r = 0; r < MAX_CLUSTER; ++r) v[r] = r < cs ? *cl.map_shared_rank(mine, r) : 0;
+#pragma unroll
+    for (int r = 0; r < MAX_CLUSTER; ++r) {
+      all += v[r];
+      low += r < rank ? v[r] : 0;
+    }
+    if (before) *before = low;
+    return all;
+  };
+
   // ---- every block of the row names one of the pool that no other row holds
   if (tid == 0) s_bad = 0;
-  hist[0][tid] = 0;
+  hist[tid] = 0;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) sums[p][tid] = 0;
   __syncthreads();
   const int blocks = (int)(((long long)L + (1 << t.bs_shift) - 1) >> t.bs_shift);
   for (int j = rank * ET + tid; j < blocks; j += cs * ET) {
@@ -132,52 +158,59 @@ __global__ void __launch_bounds__(ET) evict_kernel(const EvictArgs a) {
   // ---- the wanted-th largest weight, eight bits a pass
   uint32_t prefix = 0;
   int rest = wanted, ties = 0;
+  sync_all();                                  // every CTA's sums stand at 0
+  if (sum_of(&s_bad, nullptr) > 0) {           // the same for the whole cluster
+    if (teller) {
+      a.new_lens[i] = L;
+      atomicOr(t.err, ERR_BAD_INDEX);
+    }
+    sync_all();                                // no CTA leaves while another reads its flag
+    return;
+  }
 #pragma unroll 1
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
-    int* h = hist[pass & 1];
-    for (int p0 = c0 + warp * 32; p0 < c1; p0 += ET) {
-      const int p = p0 + lane;
-      const uint32_t key = p < c1 ? keys[p] : 0u;
+    for (int p = c0 + tid; p < c1; p += ET) {
+      const uint32_t key = keys[p];
       // 64 bits: a shift by 32 in the first pass
-      const bool in = p < c1 && ((uint64_t)(key ^ prefix) >> (shift + 8)) == 0;
-      const unsigned active = __ballot_sync(0xffffffffu, in);
-      if (in) {
-        // neighbours of one bin count together
-        const int bin = (key >> shift) & 255;
-        const unsigned same = __match_any_sync(active, bin);
-        if (lane == __ffs(same) - 1) atomicAdd(&h[bin], __popc(same));
-      }
-    }
-    cl.sync();
-    if (pass == 0) {
-      int bad = 0;
-      for (int r = 0; r < cs; ++r) bad |= *cl.map_shared_rank(&s_bad, r);
-      if (bad) {                               // the same for the whole cluster
-        if (teller) {
-          a.new_lens[i] = L;
-          atomicOr(t.err, ERR_BAD_INDEX);
-        }
-        cl.sync();                             // no CTA leaves while another reads its flag
-        return;
-      }
-    }
-    hist[(pass + 1) & 1][tid] = 0;             // read last before this barrier
-    int n = 0;
-    for (int r = 0; r < cs; ++r) n += cl.map_shared_rank(h, r)[255 - tid];
-    // thread x holds bin 255 - x: the weights of higher bins are those of lower threads
-    int all;
-    const int above = block_prefix(n, s_warp, &all);
-    if (above < rest && rest <= above + n) {
-      s_pick[0] = 255 - tid;
-      s_pick[1] = rest - above;
-      s_pick[2] = n;
+      if (((uint64_t)(key ^ prefix) >> (shift + 8)) == 0) atomicAdd(&hist[(key >> shift) & 255], 1);
     }
     __syncthreads();
-    if (wanted > 0) {
-      prefix |= (uint32_t)s_pick[0] << shift;
-      rest = s_pick[1];
-      ties = s_pick[2];
+    // Bins that are not empty go to every CTA's sums (few are: weights of a row lie
+    // within some powers of two; reading all of eight histograms took twice as long)
+    const int mine = hist[tid];
+    hist[tid] = 0;
+    if (mine > 0)
+      for (int r = 0; r < cs; ++r) atomicAdd(cl.map_shared_rank(&sums[pass][tid], r), mine);
+    sync_all();
+    // Each warp finds the bin by itself, eight bins a lane, the highest first.
+    int bin[8], n = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      bin[u] = sums[pass][BINS - 1 - 8 * lane - u];
+      n += bin[u];
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    int above = incl - n, found = 0, left = 0, there = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (above < rest && rest <= above + bin[u]) {
+        found = BINS - 1 - 8 * lane - u;
+        left = rest - above;
+        there = bin[u];
+      }
+      above += bin[u];
+    }
+    if (wanted > 0) {                          // one lane found it
+      const int src = __ffs(__ballot_sync(0xffffffffu, there > 0)) - 1;
+      prefix |= (uint32_t)__shfl_sync(0xffffffffu, found, src) << shift;
+      rest = __shfl_sync(0xffffffffu, left, src);
+      ties = __shfl_sync(0xffffffffu, there, src);
     }
   }
 
@@ -192,28 +225,13 @@ __global__ void __launch_bounds__(ET) evict_kernel(const EvictArgs a) {
   }
   __syncthreads();
   // ties: the lowest `rest` of them
-  auto count = [&](auto bits_of) {             // bits over the CTA's words
-    int n = 0;
-    for (int w = tid; w < nw; w += ET) n += __popc(bits_of(w));
-    int all;
-    (void)block_prefix(n, s_warp, &all);
-    return all;
-  };
-  auto before_me = [&](int which, int* total) {
-    int n = 0, all = 0;
-    for (int r = 0; r < cs; ++r) {
-      const int x = *cl.map_shared_rank(&s_count[which], r);
-      if (r < rank) n += x;
-      all += x;
-    }
-    *total = all;
-    return n;
-  };
   if (rest < ties) {                           // the same for the whole cluster
-    const int n = count([&](int w) { return s_eq[w]; });
-    if (tid == 0) s_count[0] = n;
-    cl.sync();
-    int all, at = before_me(0, &all);
+    int n = 0, all, at;
+    for (int w = tid; w < nw; w += ET) n += __popc(s_eq[w]);
+    (void)block_prefix(n, s_warp, &all);
+    if (tid == 0) s_count[0] = all;
+    sync_all();
+    (void)sum_of(&s_count[0], &at);
     for (int w0 = 0; w0 < nw; w0 += ET) {
       const int w = w0 + tid;
       const uint32_t eq = w < nw ? s_eq[w] : 0u;
@@ -233,37 +251,42 @@ __global__ void __launch_bounds__(ET) evict_kernel(const EvictArgs a) {
   __syncthreads();
   auto places = [&](int w) { return range_bits(base + 32 * w, lo, edge) & ~s_gt[w]; };
   auto movers = [&](int w) { return range_bits(base + 32 * w, edge, hi) & s_gt[w]; };
-  {
-    const int np = count(places), nm = count(movers);
-    if (tid == 0) { s_count[1] = np; s_count[2] = nm; }
+  // free places and movers before each word, both in one number (places in the low half)
+  int total = 0;
+  for (int w0 = 0; w0 < nw; w0 += ET) {
+    const int w = w0 + tid;
+    int here;
+    const int before =
+        block_prefix(w < nw ? __popc(places(w)) | __popc(movers(w)) << 16 : 0, s_warp, &here);
+    if (w < nw) s_eq[w] = (uint32_t)(total + before);
+    total += here;
   }
-  cl.sync();                                   // and every CTA is done with its weights
-  int moves, same;
-  int at_place = before_me(1, &moves), at_mover = before_me(2, &same);
-  // as many survivors behind the edge as places before it: both are wanted less the
-  // survivors before it
-  const int per = (moves + cs - 1) / cs;       // at most seg / 2
-  const int half = seg / 2;
-  // the lists: entry x of the cluster's is entry x % per of CTA x / per
-  auto scatter = [&](auto bits_of, int at, int off) {
-    for (int w0 = 0; w0 < nw; w0 += ET) {
-      const int w = w0 + tid;
-      uint32_t bits = w < nw ? bits_of(w) : 0u;
-      int here;
-      int x = at + block_prefix(__popc(bits), s_warp, &here);
-      for (; bits; bits &= bits - 1, ++x) {
-        const int owner = x / per;
-        cl.map_shared_rank(keys, owner)[off + x - owner * per] = base + 32 * w + __ffs(bits) - 1;
-      }
-      at += here;
+  if (tid == 0) {
+    s_count[1] = total & 0xffff;
+    s_count[2] = (int)((unsigned)total >> 16);
+  }
+  sync_all();                                  // and every CTA is done with its weights
+  int at_place, at_mover;
+  const int moves = sum_of(&s_count[1], &at_place);
+  (void)sum_of(&s_count[2], &at_mover);        // as many: both are wanted less the survivors
+                                               // before the edge
+  // the lists: entry x of the cluster's is entry x / cs of CTA x % cs, at most seg / 2
+  const int half = seg / 2, cs_shift = __ffs(cs) - 1;
+  for (int p = tid; p < seg; p += ET) {
+    const int w = p >> 5;
+    const uint32_t bit = 1u << (p & 31), mv = movers(w), pl = places(w);
+    if ((mv | pl) & bit) {
+      const bool moves_here = mv & bit;
+      const uint32_t before = s_eq[w];
+      const int x = moves_here ? at_mover + (int)(before >> 16) + __popc(mv & (bit - 1u))
+                               : at_place + (int)(before & 0xffffu) + __popc(pl & (bit - 1u));
+      cl.map_shared_rank(keys, x & (cs - 1))[(moves_here ? 0 : half) + (x >> cs_shift)] = base + p;
     }
-  };
-  scatter(movers, at_mover, 0);
-  scatter(places, at_place, half);
-  cl.sync();
+  }
+  sync_all();
 
   // ---- moves of this CTA's share: all sources lie behind the edge, all places before it
-  const int mine = max(0, min(per, moves - rank * per));
+  const int mine = (moves - rank + cs - 1) >> cs_shift;    // moves >= 0, rank < cs
   uint32_t* src = keys;
   uint32_t* dst = keys + half;
   const int bmask = (1 << t.bs_shift) - 1;
@@ -271,16 +294,23 @@ __global__ void __launch_bounds__(ET) evict_kernel(const EvictArgs a) {
     return ((uint32_t)table[p >> t.bs_shift] * (uint32_t)a.Hkv + (uint32_t)g << t.bs_shift) +
            (uint32_t)(p & bmask);
   };
+  float wt = 0.f, ks = 0.f, vs = 0.f;          // of this thread's first move
+  uint32_t to = 0;
+  int wq = -1;
   for (int x = tid; x < mine; x += ET) {
     const int p = (int)src[x], q = (int)dst[x];
-    const uint32_t from = cell(p), to = cell(q);
-    weights[q] = weights[p];
-    if (a.scale[0]) {
-      a.scale[0][to] = a.scale[0][from];
-      a.scale[1][to] = a.scale[1][from];
+    const uint32_t f = cell(p), d = cell(q);
+    src[x] = f;
+    dst[x] = d;
+    float k = 0.f, v = 0.f;
+    const float w = weights[p];
+    if (a.scale[0]) { k = a.scale[0][f]; v = a.scale[1][f]; }
+    if (x == tid) {                            // written behind the codes' loads
+      wt = w; ks = k; vs = v; to = d; wq = q;
+    } else {
+      weights[q] = w;
+      if (a.scale[0]) { a.scale[0][d] = k; a.scale[1][d] = v; }
     }
-    src[x] = from;
-    dst[x] = to;
   }
   __syncthreads();
   const int cshift = a.chunk_shift;            // 16-byte chunks of a cell in one buffer
@@ -288,21 +318,24 @@ __global__ void __launch_bounds__(ET) evict_kernel(const EvictArgs a) {
   auto chunk_of = [&](int which, uint32_t c, int k) {
     return reinterpret_cast<uint4*>(a.code[which]) + ((long long)c << cshift) + k;
   };
-  const long long chunks = (long long)mine << (cshift + 1);
-  for (long long e0 = tid; e0 < chunks; e0 += ET * MOVE_U) {
-    uint4 v[MOVE_U];
+  const int chunks = mine << (cshift + 1);     // below 2^21
+  for (int e0 = tid; e0 < chunks; e0 += ET * MOVE_U) {
+    uint4 c[MOVE_U];
 #pragma unroll
     for (int u = 0; u < MOVE_U; ++u) {
-      const long long e = e0 + u * ET;
-      if (e < chunks) v[u] = *chunk_of((int)(e >> cshift) & 1, src[e >> (cshift + 1)], (int)e & cmask);
+      const int e = e0 + u * ET;
+      if (e < chunks) c[u] = *chunk_of((e >> cshift) & 1, src[e >> (cshift + 1)], e & cmask);
     }
 #pragma unroll
     for (int u = 0; u < MOVE_U; ++u) {
-      const long long e = e0 + u * ET;
-      if (e < chunks) *chunk_of((int)(e >> cshift) & 1, dst[e >> (cshift + 1)], (int)e & cmask) = v[u];
+      const int e = e0 + u * ET;
+      if (e < chunks) *chunk_of((e >> cshift) & 1, dst[e >> (cshift + 1)], e & cmask) = c[u];
     }
   }
-  cl.sync();                                   // what moved has been read
+  if (wq >= 0) {
+    weights[wq] = wt;
+    if (a.scale[0]) { a.scale[0][to] = ks; a.scale[1][to] = vs; }
+  }
 
   // ---- the last cells, in order.  Where old and new places overlap one CTA takes
   // them, a round at a time: all of a round is read before any of it is written
@@ -311,11 +344,10 @@ __global__ void __launch_bounds__(ET) evict_kernel(const EvictArgs a) {
   const int share = apart ? (a.last + cs - 1) / cs : (rank == 0 ? a.last : 0);
   const int r0 = apart ? min(a.last, rank * share) : 0, r1 = min(a.last, r0 + share);
   const int round = max(1, (ET * MOVE_U) >> (cshift + 1));   // cells, at most 2 ET
-  for (int x0 = r0; x0 < r1; x0 += round) {
-    const int cells = min(round, r1 - x0);
-    const int nch = cells << (cshift + 1);
+  for (int x0 = r0; x0 == r0 || x0 < r1; x0 += round) {
+    const int cells = min(round, r1 - x0), nch = cells << (cshift + 1);   // <= 0: none here
     uint4 v[MOVE_U];
-    float wt[2], k[2], s[2];
+    float rw[2], rk[2], rv[2];
 #pragma unroll
     for (int u = 0; u < MOVE_U; ++u) {
       const int e = tid + u * ET;
@@ -325,12 +357,14 @@ __global__ void __launch_bounds__(ET) evict_kernel(const EvictArgs a) {
     for (int u = 0; u < 2; ++u) {
       const int x = tid + u * ET;
       if (x < cells) {
-        const uint32_t from = cell(hi + x0 + x);
-        wt[u] = weights[hi + x0 + x];
-        if (a.scale[0]) { k[u] = a.scale[0][from]; s[u] = a.scale[1][from]; }
+        const uint32_t f = cell(hi + x0 + x);
+        rw[u] = weights[hi + x0 + x];
+        if (a.scale[0]) { rk[u] = a.scale[0][f]; rv[u] = a.scale[1][f]; }
       }
     }
-    __syncthreads();
+    // the round has been read; before the first write, everything that moved above too
+    if (x0 == r0) sync_all();
+    else __syncthreads();
 #pragma unroll
     for (int u = 0; u < MOVE_U; ++u) {
       const int e = tid + u * ET;
@@ -340,14 +374,13 @@ __global__ void __launch_bounds__(ET) evict_kernel(const EvictArgs a) {
     for (int u = 0; u < 2; ++u) {
       const int x = tid + u * ET;
       if (x < cells) {
-        const uint32_t to = cell(edge + x0 + x);
-        weights[edge + x0 + x] = wt[u];
-        if (a.scale[0]) { a.scale[0][to] = k[u]; a.scale[1][to] = s[u]; }
+        const uint32_t d = cell(edge + x0 + x);
+        weights[edge + x0 + x] = rw[u];
+        if (a.scale[0]) { a.scale[0][d] = rk[u]; a.scale[1][d] = rv[u]; }
       }
     }
-    __syncthreads();
   }
-  cl.sync();                                   // the weights behind the new end have been read
+  sync_all();                                  // the weights behind the new end have been read
   for (int p = keep + rank * ET + tid; p < L; p += cs * ET) weights[p] = 0.f;
   if (teller) a.new_lens[i] = keep;
 }
