@@ -60,12 +60,19 @@ struct Shape {
   static constexpr int NB = D / 64;                        // 64-d blocks of a row
   static constexpr int QB = ROWS * D * 2;                  // bytes of a query tile
   static constexpr int SLOT = KT * D * 2;                  // and of a K or V tile
+  // With one query tile Q lives in tensor memory, the A operand of S: there its MMAs of
+  // 64 keys would read more of Q from shared memory than of K, and its place there
+  // holds two more tiles of K and V.  It passes through two slots of the ring.
+  static constexpr bool QTM = NQ == 1;
+  static constexpr int QSM = QTM ? 0 : NQ * QB;
+  static constexpr int QCOL = 384;
+  static_assert(!QTM || (QB == 2 * SLOT && QCOL + D / 2 <= 512), "queries in two slots");
   static constexpr int AUX = 512;                          // items and barriers
   static constexpr int SOFT = 4 * NQ;                      // softmax warps
   static constexpr int OUT = SOFT * 32 * 128;              // 64 elements of their rows on the way out
   static constexpr int LIMIT = 232448 - 1024 - AUX - OUT;  // shared memory, less alignment
-  static constexpr int NS = (LIMIT - NQ * QB) / SLOT < 8 ? (LIMIT - NQ * QB) / SLOT : 8;
-  static constexpr int SMEM = NQ * QB + NS * SLOT + OUT + AUX + 1024;
+  static constexpr int NS = (LIMIT - QSM) / SLOT < 8 ? (LIMIT - QSM) / SLOT : 8;
+  static constexpr int SMEM = QSM + NS * SLOT + OUT + AUX + 1024;
   static constexpr int PROD = SOFT, MMA = SOFT + 1;
   static constexpr int THREADS = (SOFT + 4) * 32;
   __host__ __device__ static constexpr int scol(int j, int b) { return NQ == 2 ? 128 * j : 256 + KT * b; }
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* qsm = smem;                                     // NQ query tiles
-  uint8_t* ring = smem + NQ * C::QB;                       // NS slots
+  uint8_t* ring = smem + C::QSM;                           // NS slots
   uint8_t* outs = ring + NS * C::SLOT;                     // 4 KB per softmax warp
   uint8_t* answer = outs + C::OUT;                         // 16 bytes
   volatile Item* items = reinterpret_cast<volatile Item*>(answer + 16);   // [2]
@@ -133,7 +140,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
   uint64_t* asked = empty + NS;                            // the answer is there
   uint64_t* item_full = asked + 1;                         // [2] producer -> MMA, softmax
   uint64_t* item_empty = item_full + 2;                    // [2] MMA, softmax -> producer
-  uint64_t* q_full = item_empty + 2;                       // producer -> MMA
+  uint64_t* q_full = item_empty + 2;                       // producer, or softmax (QTM) -> MMA
   uint64_t* q_empty = q_full + 1;                          // MMA (commit) -> producer
   uint64_t* s_full = q_empty + 1;                          // [NQ][SB] MMA (commit) -> softmax
   uint64_t* p_full = s_full + NQ * SB;                     // [NQ][SB] softmax -> MMA
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
       mbar_init(&item_full[s], 1);
       mbar_init(&item_empty[s], C::SOFT + 1);
     }
-    mbar_init(q_full, 1);
+    mbar_init(q_full, C::QTM ? 128 : 1);
     mbar_init(q_empty, 1);
     for (int s = 0; s < NQ * SB; ++s) {
       mbar_init(&s_full[s], 1);
@@ -305,19 +312,37 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
       int loaded = 0;                                      // items whose Q was loaded
       for (bool go = publish(); go && it.p0 >= 0; go = publish()) {
         const int nqt = query_tiles(it), kt0 = first_tile(it), ntl = tiles_of(it, nqt - 1);
-        for (int i = 0; go && i < SB && i < ntl; ++i) go = load(&kmap, (kt0 + i) * KT);
-        if (go && k >= 1) go = wait(q_empty, (uint32_t)((k - 1) & 1));
-        if (!go) break;
-        if (elect_one()) {
-          mbar_expect_tx(q_full, nqt * C::QB);
-          for (int j = 0; j < nqt; ++j)
+        if constexpr (C::QTM) {
+          for (int half = 0; go && half < 2; ++half) {
+            const int slot = issued % NS;
+            if (issued >= NS) go = wait(&empty[slot], (uint32_t)((issued / NS - 1) & 1));
+            if (!go) break;
+            if (elect_one()) {
+              mbar_expect_tx(&full[slot], C::SLOT);
 #pragma unroll
-            for (int c = 0; c < C::NB; ++c)
-              tma_tile_3d(qsm + j * C::QB + c * (ROWS * 128), &qmap, 128 * c, it.g << a.g_shift,
-                          it.t0 + it.p0 + j * QP, q_full);
+              for (int c = 0; c < C::NB / 2; ++c)
+                tma_tile_3d(ring + slot * C::SLOT + c * (ROWS * 128), &qmap, 128 * (half * (C::NB / 2) + c),
+                            it.g << a.g_shift, it.t0 + it.p0, &full[slot]);
+            }
+            __syncwarp();
+            ++issued;
+          }
         }
-        __syncwarp();
-        ++loaded;
+        for (int i = 0; go && i < SB && i < ntl; ++i) go = load(&kmap, (kt0 + i) * KT);
+        if constexpr (!C::QTM) {
+          if (go && k >= 1) go = wait(q_empty, (uint32_t)((k - 1) & 1));
+          if (!go) break;
+          if (elect_one()) {
+            mbar_expect_tx(q_full, nqt * C::QB);
+            for (int j = 0; j < nqt; ++j)
+#pragma unroll
+              for (int c = 0; c < C::NB; ++c)
+                tma_tile_3d(qsm + j * C::QB + c * (ROWS * 128), &qmap, 128 * c, it.g << a.g_shift,
+                            it.t0 + it.p0 + j * QP, q_full);
+          }
+          __syncwarp();
+          ++loaded;
+        }
         for (int i = 0; go && i < ntl; ++i) {
           if (i == max(0, ntl - 2) && elect_one()) {       // the next item, no earlier than needed
             mbar_expect_tx(asked, 16);
@@ -377,9 +402,11 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
           if (elect_one()) {
             tc_fence_after();
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-              umma(td, qa + (uint64_t)((((s >> 2) * (ROWS * 128)) + (s & 3) * 32) >> 4),
-                   kb + (uint64_t)((((s >> 2) * (KT * 128)) + (s & 3) * 32) >> 4), id, s > 0);
+            for (int s = 0; s < D / 16; ++s) {
+              const uint64_t b = kb + (uint64_t)((((s >> 2) * (KT * 128)) + (s & 3) * 32) >> 4);
+              if constexpr (C::QTM) umma_tmem_a(td, tmem + C::QCOL + 8 * s, b, id, s > 0);
+              else umma(td, qa + (uint64_t)((((s >> 2) * (ROWS * 128)) + (s & 3) * 32) >> 4), b, id, s > 0);
+            }
             umma_commit(&s_full[j * SB + sb]);
           }
           __syncwarp();
@@ -406,6 +433,14 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
           __syncwarp();
         };
         go = wait(q_full, (uint32_t)(k & 1));
+        if constexpr (C::QTM) {                            // its slots have been read
+          if (lane == 0) {
+            mbar_arrive(&empty[x % NS]);
+            mbar_arrive(&empty[(x + 1) % NS]);
+          }
+          __syncwarp();
+          x += 2;
+        }
         int slot = 0;
         for (int i = 0; go && i < SB && i < ntl; ++i) {
           go = take(slot);
@@ -475,9 +510,48 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
     const float c = a.qk_scale;
     int used = 0, items_done = 0;
     bool ok = true;
-    Item it;
-    for (int k = 0; ok && take_item(k, it); ++k) {
-      if (j >= query_tiles(it)) continue;
+    // QTM: this thread's row of Q, from the ring's entry `at` and the next into tensor
+    // memory (the scores before, which read the one that was there, are complete)
+    int at = 0;
+    auto copy_queries = [&]() -> bool {
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int slot = (at + half) % NS;
+        if (!wait(&full[slot], (uint32_t)(((at + half) / NS) & 1))) return false;
+#pragma unroll 1
+        for (int b = 0; b < C::NB / 2; ++b) {
+          const uint8_t* block = ring + slot * C::SLOT + b * (ROWS * 128);
+          const uint32_t to = trow + C::QCOL + (half * (C::NB / 2) + b) * 32;
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            uint32_t w[16];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint4 v = *reinterpret_cast<const uint4*>(block + swc(r, e + y));
+              w[4 * y] = v.x; w[4 * y + 1] = v.y; w[4 * y + 2] = v.z; w[4 * y + 3] = v.w;
+            }
+            tmem_st16_nowait(to + 4 * e, w);
+          }
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(q_full);
+      return true;
+    };
+    Item it, next;
+    bool more = false;
+    if constexpr (C::QTM) {
+      more = take_item(0, it);
+      if (more) ok = copy_queries();
+    }
+    for (int k = 0; ok; ++k) {
+      if constexpr (C::QTM) {
+        if (!more) break;
+      } else {
+        if (!take_item(k, it)) break;
+        if (j >= query_tiles(it)) continue;
+      }
       const int kt0 = first_tile(it), nt = tiles_of(it, j);
       const int pos = it.p0 + off;
       const int lo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
@@ -576,6 +650,11 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
         mbar_arrive(&p_full[sb]);
       }
       used += nt;
+      if constexpr (C::QTM) {                              // the next item's queries, meanwhile
+        at += 2 + 2 * nt;
+        if (ok) more = take_item(k + 1, next);
+        if (ok && more) ok = copy_queries();
+      }
       // ---- epilogue: O / l
       if (ok) ok = wait(&o_full[j], (uint32_t)(items_done & 1));
       if (!ok) break;
@@ -618,6 +697,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
         }
         __syncwarp();
       }
+      if constexpr (C::QTM) it = next;
     }
   }
 
