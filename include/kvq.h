@@ -589,12 +589,12 @@ kvq_status kvq_prompt_attention(const kvq_ctx* ctx, int layer, const void* q,
  *   of no group read all of their positions.  shared_lens: device int32 [num_groups].
  *   num_groups 0: both may be NULL.
  * max_group: an upper bound of a group's rows; the rows of a larger group read the
- *   prefix each for itself (so do groups of one row).
+ *   prefix each for itself, as do those of groups so small, or behind prefixes so
+ *   short, that a pass for all would take longer (decided on the device).
  * max_shared, max_own: upper bounds of shared_lens and of a row's positions behind
  *   its prefix, for the plan only.
- * num_splits, workspace: from kvq_shared_prefix_plan with the same sizes; num_splits 0
- *   = the plan's choice.  The workspace (16-byte aligned) needs no initialisation;
- *   overlapping calls need one each.
+ * num_splits, workspace: as for kvq_shared_prefix_plan, with the same sizes.  The
+ *   workspace (16-byte aligned) needs no initialisation; overlapping calls need one each.
  * Softmax and sums are fp32; over the prefix, the weight that meets a V code is
  * rounded as kvq_cross_attention says.  A layer with a window is
  * KVQ_ERR_UNSUPPORTED (it reads no long prefix).  Starts that descend or leave
@@ -611,11 +611,11 @@ kvq_status kvq_shared_prefix_attention(const kvq_ctx* ctx, int layer, const void
                                        int max_shared, int max_own, void* out, int num_splits,
                                        void* workspace, size_t workspace_bytes, void* stream);
 
-/* Splits of a prefix at most, and workspace bytes, of a kvq_shared_prefix_attention call:
- * on input *num_splits > 0 (at most 1024) requests a bound, 0 asks for the plan's; on
- * output it is 0 where nothing can be shared (no group of two rows, or no prefix of 16
- * positions).  How the prefixes are cut within it is decided on the device, from their
- * lengths. */
+/* Workspace bytes of a kvq_shared_prefix_attention call.  *num_splits 0: whether a
+ * prefix is shared, and in how many splits over the SMs, is decided on the device from
+ * the lengths.  > 0 (at most 1024): every prefix of at least 16 positions with two rows
+ * is shared, in so many splits at most.  On output *num_splits is what it was, or 0
+ * where nothing can be shared. */
 kvq_status kvq_shared_prefix_plan(const kvq_ctx* ctx, int layer, int batch, int num_groups,
                                   int max_group, int max_shared, int max_own, int* num_splits,
                                   size_t* workspace_bytes);

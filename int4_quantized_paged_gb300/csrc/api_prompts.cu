@@ -107,7 +107,13 @@ kvq_status plan_shared(const kvq_ctx* ctx, int layer, int batch, int num_groups,
   const kvq_config& c = ctx->cfg;
   if (max_group > batch) max_group = batch;
   *p = {};
-  if (num_groups > 0 && max_group > 1 && max_shared >= 16) {
+  bool share = num_groups > 0 && max_group > 1 && max_shared >= 16;
+  // nothing to gain, were every row to share the longest prefix (the device's own test
+  // would only find so behind the launch of the pass, some 4 us)
+  if (num_splits == 0 && 2.0 * batch * ((max_shared + 63) / 64) * c.num_kv_heads <
+                             5.0 * (SHARED_PASS + 4) * sm_count())
+    share = false;
+  if (share) {
     const int tile = cross_query_tile(c.head_dim, c.num_q_heads / c.num_kv_heads);
     // units of one split, in steps whose products fit 64 bits
     const long long base = ((long long)max_group + tile - 1) / tile * num_groups;
@@ -125,9 +131,9 @@ kvq_status plan_shared(const kvq_ctx* ctx, int layer, int batch, int num_groups,
     if (units >= (1LL << 34) / p->unit_rows / c.num_q_heads) return KVQ_ERR_INVALID_ARG;
     p->rows = (size_t)units * p->unit_rows * c.num_q_heads;
   }
-  // a prefix is cut to whole tiles of 16, and what is left over is a row's own
+  // a row that reads its prefix alone has all of its positions as its own
   int workers = 0;
-  st = kvq_decode_plan(ctx, layer, batch, max_own + 15, &workers, nullptr);
+  st = kvq_decode_plan(ctx, layer, batch, max_shared + max_own, &workers, nullptr);
   if (st != KVQ_OK) return st;
   p->workers = workers;
   p->index_bytes = align16(((size_t)batch * 2 + (size_t)num_groups * 3 + 1) * sizeof(int));
@@ -194,7 +200,7 @@ kvq_status kvq_shared_prefix_plan(const kvq_ctx* ctx, int layer, int batch, int 
   const kvq_status st = plan_shared(ctx, layer, batch, num_groups, max_group, max_shared, max_own,
                                     *num_splits, &p);
   if (st != KVQ_OK) return st;
-  *num_splits = p.splits;
+  if (p.units == 0) *num_splits = 0;
   if (workspace_bytes) *workspace_bytes = p.bytes();
   return KVQ_OK;
 }
@@ -229,7 +235,7 @@ kvq_status kvq_shared_prefix_attention(const kvq_ctx* ctx, int layer, const void
   a.err = error_word();
   if (!a.err) return KVQ_ERR_CUDA;
   a.workers = p.workers;
-  a.stream_once = stream_once(ctx, layer, batch, max_own);
+  a.stream_once = stream_once(ctx, layer, batch, (long long)max_shared + max_own);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   SharedArgs x = {};
   x.group_start = group_start;
@@ -237,6 +243,7 @@ kvq_status kvq_shared_prefix_attention(const kvq_ctx* ctx, int layer, const void
   x.groups = num_groups;
   x.max_group = max_group < batch ? max_group : batch;
   x.max_splits = p.splits;
+  x.always = num_splits > 0;
   x.max_units = p.units;
   x.unit_rows = p.unit_rows;
   x.tile = cross_query_tile(c.head_dim, c.num_q_heads / c.num_kv_heads);

@@ -149,6 +149,9 @@ struct EvictArgs {
   int seg_max;                 // set by the launcher: cells of a CTA at most
 };
 
+// What a pass over shared prefixes costs beside its key tiles, in key tiles.
+constexpr int SHARED_PASS = 10;
+
 // Decode behind shared prefixes (beside DecodeArgs).  A unit is a split of a group's
 // prefix against a query tile of its rows, for every KV head.
 struct SharedArgs {
@@ -156,6 +159,7 @@ struct SharedArgs {
   const int* shared_lens;      // [groups]
   int groups, max_group;
   int max_splits;              // of one prefix
+  int always;                  // share what can be, whether it gains or not
   int max_units, unit_rows;    // units, and rows of each, that there is room for
   int tile;                    // rows of a query tile
   int sms;

@@ -32,10 +32,18 @@ namespace kvq {
 namespace {
 
 constexpr int PT = 1024;
-constexpr int MIN_ROWS = 2;                    // rows of a group that are worth a shared pass
+// What sharing costs and saves, in the time that a CTA takes for a key tile (64 keys of
+// one KV head against a query tile, about 0.9 us).  The decode kernel reads 160 keys of
+// a row and KV head for an SM in that time, so a group gains from three rows on (times
+// its keys: 1 against 0.4 a row); the pass itself, and the join of its splits, cost
+// about ten more (SHARED_PASS).  Measured, FP8, 32 heads of 128, 64 rows, shared / each row for
+// itself: 32 groups of 2 behind 4,096 positions 134 / 91 us, 16 of 4 85 / 90, 8 of 8
+// 58 / 90; 8 groups of 8 behind 512 positions 36 / 27; one group of 64 behind 32,768
+// 112 / 613.
+constexpr int MIN_ROWS = 3;
 
 __global__ void __launch_bounds__(PT) plan_kernel(const DecodeArgs a, const SharedArgs x) {
-  __shared__ unsigned long long s_best;
+  __shared__ unsigned long long s_best, s_alone;
   __shared__ int s_most;
   for (int b = threadIdx.x; b < a.B; b += PT) {
     x.first[b] = 0;
@@ -43,6 +51,7 @@ __global__ void __launch_bounds__(PT) plan_kernel(const DecodeArgs a, const Shar
   }
   if (threadIdx.x == 0) {
     s_best = ~0ull;
+    s_alone = 0;
     s_most = 0;
   }
   // starts that do not ascend within the batch might put a row into two groups
@@ -54,33 +63,31 @@ __global__ void __launch_bounds__(PT) plan_kernel(const DecodeArgs a, const Shar
   astray = __syncthreads_or(astray);
   if (astray && threadIdx.x == 0) atomicOr(a.err, ERR_BAD_INDEX);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int least_rows = x.always ? 2 : MIN_ROWS;
   for (int g = warp; g < x.groups; g += PT / 32) {
     const int r0 = x.group_start[g], r1 = x.group_start[g + 1], P = x.shared_lens[g];
     if (P < 0 && lane == 0) atomicOr(a.err, ERR_BAD_INDEX);
     int shared = 0;
-    // rows past the caller's bound, and a row by itself, read their prefix alone
-    if (!astray && P > 0 && x.max_units > 0 && r1 - r0 >= MIN_ROWS && r1 - r0 <= x.max_group) {
+    // rows past the caller's bound, and few rows, read their prefix alone
+    if (!astray && P > 0 && x.max_units > 0 && r1 - r0 >= least_rows && r1 - r0 <= x.max_group) {
       shared = P;
       for (int b = r0 + lane; b < r1; b += 32) shared = min(shared, ctx_len(a, b));
       shared = __reduce_min_sync(0xffffffffu, shared) & ~(TILE - 1);
     }
     if (lane == 0) {
+      const int tiles = (shared + CROSS_KEYS - 1) / CROSS_KEYS;
       x.prefix[g] = shared;
-      atomicMax(&s_most, (shared + CROSS_KEYS - 1) / CROSS_KEYS);
+      atomicMax(&s_most, tiles);
+      atomicAdd(&s_alone, (unsigned long long)tiles * (unsigned)max(r1 - r0, 0));
     }
-    if (shared > 0)
-      for (int b = r0 + lane; b < r1; b += 32) {
-        x.first[b] = shared;
-        x.group_of[b] = g;
-      }
   }
   __syncthreads();
   const int most = s_most;
-  if (most == 0) {                             // nothing is shared
+  if (most == 0) {                             // nothing to share
     if (threadIdx.x == 0) *x.num_units = 0;
     return;
   }
-  // Query tiles and key tiles of a group (its rows were checked above).
+  // Query tiles and key tiles of a group.
   auto sizes = [&](int g, int* tiles) {
     *tiles = (x.prefix[g] + CROSS_KEYS - 1) / CROSS_KEYS;
     return *tiles > 0 ? (x.group_start[g + 1] - x.group_start[g] + x.tile - 1) / x.tile : 0;
@@ -102,6 +109,19 @@ __global__ void __launch_bounds__(PT) plan_kernel(const DecodeArgs a, const Shar
   }
   __syncthreads();
   const int per = 0x7fffffff - (int)(s_best & 0x7fffffffu);
+  // 5 (cost + SHARED_PASS) SMs < 2 KV heads x rows x key tiles: 0.4 of a tile each
+  if (!x.always && 5 * ((s_best >> 31) + SHARED_PASS) * (unsigned)x.sms >= 2 * s_alone * (unsigned)a.Hkv) {
+    if (threadIdx.x == 0) *x.num_units = 0;
+    return;
+  }
+  for (int g = warp; g < x.groups; g += PT / 32) {
+    const int shared = x.prefix[g];
+    if (shared > 0)
+      for (int b = x.group_start[g] + lane; b < x.group_start[g + 1]; b += 32) {
+        x.first[b] = shared;
+        x.group_of[b] = g;
+      }
+  }
   // The list of units: a group's query tiles are neighbours, so that they read its pages
   // from L2.
   if (warp == 0) {

@@ -502,7 +502,7 @@ def kvq_prompt_attention(ctx: Context, layer: int, q, k, v, seq_start, out, *, m
 
 def kvq_shared_prefix_plan(ctx: Context, layer: int, batch: int, num_groups: int, *, max_group: int,
                            max_shared: int, max_own: int, num_splits: int = 0):
-    """(splits of the prefixes, workspace bytes)."""
+    """(num_splits as the call takes it, workspace bytes)."""
     s, w = i32(num_splits), sz()
     _check(_lib.kvq_shared_prefix_plan(ctx.handle, layer, batch, num_groups, max_group, max_shared, max_own,
                                        ctypes.byref(s), ctypes.byref(w)), "kvq_shared_prefix_plan")

@@ -116,7 +116,7 @@ def test_a_servers_day(mode, D, Hkv):
     batch = [0, 2, 3, 1]
     start, shared = _i32([0, 3]), _i32([130])
     sizes = dict(max_group=3, max_shared=130, max_own=160)
-    splits, need = kvq.kvq_shared_prefix_plan(s.ctx, 0, 4, 1, **sizes)
+    splits, need = kvq.kvq_shared_prefix_plan(s.ctx, 0, 4, 1, num_splits=2, **sizes)
     work = torch.empty(need, dtype=torch.uint8, device="cuda")
     for step in range(20):
         x = s.grow(batch, [1] * 4)

@@ -63,7 +63,8 @@ class Case:
         self.most = max([b - a for a, b in zip(self.start, self.start[1:])], default=0)
         self.max_own = max([n - p for n, p in zip(self.lens, prefix)] + [0])
 
-    def run(self, splits=0, stream=None, out=None, work=None, groups=None, **kw):
+    def run(self, splits=8, stream=None, out=None, work=None, groups=None, **kw):
+        """splits 8: shared whether it gains or not; 0: the device's choice."""
         a = dict(max_group=self.most, max_shared=max(self.shared, default=0), max_own=self.max_own)
         a.update(kw)
         NG = len(self.shared) if groups is None else groups
@@ -118,16 +119,20 @@ def test_block_sizes(mode, bs):
 def test_rows_of_a_group(mode, rows):
     """One query tile in its forms, and more than one pair of them."""
     c = Case(mode, 128, 16, 2, [(500, [1 + i % 20 for i in range(rows)])], seed=rows)
-    c.run()
-    c.check()
+    for splits in (8, 0):
+        c.out.fill_(7.0)
+        c.run(splits)
+        c.check()
 
 
 @pytest.mark.parametrize("mode", MODES)
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_long_prefix(mode, D):
     c = Case(mode, D, 4, 2, [(20000, [3, 100, 1]), (12345, [2, 900])], seed=5)
-    assert c.run() > 1
-    c.check()
+    for splits in (0, 1, 40):
+        c.out.fill_(7.0)
+        c.run(splits)
+        c.check()
 
 
 def test_a_row_shorter_than_the_prefix():
@@ -140,8 +145,10 @@ def test_a_row_shorter_than_the_prefix():
 def test_sizes_that_the_caller_underestimates():
     """max_shared and max_own size the plan only; a group past max_group is read row by row."""
     c = Case(2, 128, 8, 2, [(900, [5, 400]), (500, [1, 2, 3, 4])], seed=7)
-    c.run(splits=3, max_shared=100, max_own=1)
-    c.check()
+    for splits in (3, 0):
+        c.out.fill_(7.0)
+        c.run(splits, max_shared=100, max_own=1)
+        c.check()
     c.out.fill_(7.0)
     c.run(max_group=3)
     c.check()
@@ -170,12 +177,13 @@ def test_bad_groups_share_nothing():
 
 def test_many_groups():
     """More groups than SMs, of all lengths; and one long prefix among short ones."""
-    c = Case(3, 64, 4, 2, [(1 + (37 * i) % 300, [1 + i % 5, 2]) for i in range(170)], seed=20)
-    c.run()
-    c.check()
-    c = Case(1, 128, 8, 2, [(40, [1, 2]), (9000, [3, 1, 1]), (70, [5, 5]), (1, [2, 2])], seed=21)
-    c.run()
-    c.check()
+    for c in (Case(3, 64, 4, 2, [(1 + (37 * i) % 300, [1 + i % 5, 2]) for i in range(170)], seed=20),
+              Case(1, 128, 8, 2, [(40, [1, 2]), (9000, [3, 1, 1]), (70, [5, 5]), (1, [2, 2])], seed=21),
+              Case(3, 128, 8, 2, [(20000, [5] * 40), (16, [1, 2]), (3000, [7, 2])], seed=22)):
+        for splits in (0, 1, 5, 1024):
+            c.out.fill_(7.0)
+            c.run(splits)
+            c.check()
 
 
 def test_lengths_and_blocks_out_of_range():

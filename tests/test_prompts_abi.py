@@ -19,14 +19,16 @@ def _plan(ctx=None, layer=0, batch=16, groups=2, splits=0, **kw):
 
 def test_shared_plan():
     splits, need = _plan()
-    assert splits >= 1 and need % 16 == 0
+    assert splits == 0 and need % 16 == 0            # the device's choice stays that
+    assert need < _plan(splits=1)[1]                 # too little to gain from: no room for partials
+    assert _plan(max_shared=200000)[1] >= _plan(splits=1, max_shared=200000)[1]
     # two groups, a unit for each split: its entry, and a partial of 8 rows
     assert _plan(splits=7)[1] - _plan(splits=5)[1] == 2 * 2 * (16 + 8 * 32 * 129 * 4)
     assert _plan(splits=7)[0] == 7
     # nothing to share: no splits and no room for them
     for kw in (dict(groups=0), dict(max_group=1), dict(max_shared=15), dict(batch=1)):
-        assert _plan(**kw)[0] == 0
-        assert _plan(**kw)[1] < _plan(splits=1)[1]
+        assert _plan(splits=3, **kw)[0] == 0
+        assert _plan(splits=3, **kw)[1] < _plan(splits=1)[1]
     assert _plan(max_group=500)[1] == _plan(max_group=16)[1]         # no group has more rows than the batch
 
 
