@@ -11,7 +11,10 @@
  * Around them: the work plan of the decode (kvq_decode_plan), its variants
  * (bf16 output, FP8 query, no caller workspace), prefill attention over the
  * same cache (kvq_prefill_attention), static per-head calibration, the
- * capacity accounting of the pages and the device codec on its own.
+ * capacity accounting of the pages and the device codec on its own; rotary
+ * positions, the pages of the pool and cross attention; and for long and shared
+ * prompts: attention before anything is cached, decode behind a shared prefix,
+ * decode with accumulated weights and the eviction that goes by them.
  *
  * The operations and their scale layouts follow three pages:
  *   [P1] "Per-tensor vs per-head FP8 KV cache scales"
@@ -741,7 +744,7 @@ kvq_status kvq_e4m3_encode(const float* in, unsigned char* out, long long n, voi
 kvq_status kvq_get_device_error(void* stream);
 
 /* Check of the timeout path (no counterpart on the pages).  Every wait of the
- * decode, prefill, cross and staged cache-write kernels on a shared-memory barrier
+ * decode, prefill, cross, prompt and staged cache-write kernels on a shared-memory barrier
  * is bounded (about 2 s); a wait that runs out sets the TIMEOUT bit of the
  * device error word and the kernel stops instead of hanging the GPU.  This
  * call enqueues one warp that waits in the same way on a barrier that expects

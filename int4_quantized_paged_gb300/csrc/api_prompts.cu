@@ -273,6 +273,7 @@ kvq_status kvq_decode_weights_plan(const kvq_ctx* ctx, int layer, int batch, int
   st = kvq_decode_plan(ctx, layer, batch, max_context, num_workers, nullptr);
   if (st != KVQ_OK) return st;
   const kvq_config& c = ctx->cfg;
+  if ((double)batch * c.num_q_heads * (double)max_context >= 0x1p60) return KVQ_ERR_INVALID_ARG;
   // partials, the rows' log2 sums, and the scores
   if (workspace_bytes)
     *workspace_bytes = partial_bytes(c, batch, *num_workers) +

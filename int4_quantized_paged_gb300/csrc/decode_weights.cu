@@ -11,7 +11,9 @@
 //
 // What bounds it: the decode's bytes, and 8 G + 8 more for each position and KV head
 // (scores written and read, of which the L2 holds the read ones of small batches; a
-// weight read and written).
+// weight read and written).  64 rows of 1,500-4,200 positions, 32 heads of 128, FP8 per
+// token and head: 79.5 us, 5.1 TB/s, where the decode without weights takes 68.5; 4 rows
+// of 20,000-40,000, 64 heads of 64, BF16: 62.5 and 59.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -17,11 +17,14 @@
 //  * the warp-specialised attention of cross.cu over the units: rows x heads on the
 //    tensor cores;
 //  * the decode kernel over the rows' own positions, which begins while the prefixes'
-//    last CTAs run (it does not read their results);
+//    last CTAs run (it does not read their results; the prefixes' launch itself gains
+//    nothing from being one of that kind);
 //  * join_kernel: all partials of a row.
 //
 // What bounds it: the prefix's bytes for few rows, 4 D flops per row, head and prefix
-// position for many.
+// position for many.  One group of 64 rows behind 32,768 positions, 64 heads of 128, FP8
+// per head, up to 1,000 positions of their own: 112 us (prefix 72, 930 TFLOP/s; own
+// positions 31, partly beside it; join 9; plan 5).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -39,7 +42,7 @@ constexpr int PT = 1024;
 // about ten more (SHARED_PASS).  Measured, FP8, 32 heads of 128, 64 rows, shared / each row for
 // itself: 32 groups of 2 behind 4,096 positions 134 / 91 us, 16 of 4 85 / 90, 8 of 8
 // 58 / 90; 8 groups of 8 behind 512 positions 36 / 27; one group of 64 behind 32,768
-// 112 / 613.
+// (64 heads, scales per head) 114 / 570.
 constexpr int MIN_ROWS = 3;
 
 __global__ void __launch_bounds__(PT) plan_kernel(const DecodeArgs a, const SharedArgs x) {

@@ -117,7 +117,8 @@ def test_weights_plan():
         _weights(wsb=need - 1)
     one = kvq.kvq_decode_weights_plan(_ctx(), 0, 16, 4096, 1)[1]      # the scores need it with one worker too
     assert one >= 16 * 32 * 4096 * 4
-    for bad in (dict(layer=2), dict(batch=-1), dict(most=-1), dict(workers=-1)):
+    for bad in (dict(layer=2), dict(batch=-1), dict(most=-1), dict(workers=-1),
+                dict(batch=(1 << 31) - 1, most=(1 << 31) - 1)):
         a = dict(layer=0, batch=2, most=100, workers=0)
         a.update(bad)
         with pytest.raises(kvq.KVQError, match="INVALID_ARG"):
