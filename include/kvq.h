@@ -561,7 +561,8 @@ kvq_status kvq_cross_plan(const kvq_ctx* ctx, int layer, int batch, int max_quer
  *   past it set KVQ_ERR_BAD_INDEX on the device word and are not computed.
  * num_tokens: tokens that q, k, v and out hold, below 2^31 - 256.  A sequence with a
  *   negative start or length, or past num_tokens, sets KVQ_ERR_BAD_INDEX; its rows
- *   stay as they are.
+ *   stay as they are.  (Behind starts that descend a token can be in two sequences;
+ *   its row of out is then undefined.)
  * out: bf16 [num_tokens][Hq][D], 16-byte aligned; it overlaps none of q, k and v.
  * Scores, softmax statistics and sums are fp32; the weight that meets v, relative
  * to the row's largest (to within 2^8), is rounded to bf16, as the output is.
@@ -594,8 +595,8 @@ kvq_status kvq_prompt_attention(const kvq_ctx* ctx, int layer, const void* q,
  * max_group: an upper bound of a group's rows; the rows of a larger group read the
  *   prefix each for itself, as do those of groups so small, or behind prefixes so
  *   short, that a pass for all would take longer (decided on the device).
- * max_shared, max_own: upper bounds of shared_lens and of a row's positions behind
- *   its prefix, for the plan only.
+ * max_shared, max_own: upper bounds (below 2^30) of shared_lens and of a row's
+ *   positions behind its prefix, for the plan only.
  * num_splits, workspace: as for kvq_shared_prefix_plan, with the same sizes.  The
  *   workspace (16-byte aligned) needs no initialisation; overlapping calls need one each.
  * Softmax and sums are fp32; over the prefix, the weight that meets a V code is
@@ -679,7 +680,8 @@ kvq_status kvq_decode_weights_plan(const kvq_ctx* ctx, int layer, int batch, int
  * rows, keep_lens: device int32 [num_rows]; a row at most once.
  * new_lens: device int32 [num_rows], written: min(L, keep_lens[i]), or L for a row
  *   that is refused (below), or 0 where rows[i] itself is (kvq_truncate_sequences
- *   refuses it then, too).
+ *   refuses it then, too).  It overlaps neither context_lens nor rows; it may be
+ *   keep_lens itself.
  * ref_count: as for the page calls, read only, or NULL where the caller keeps none.
  *   With it, a row of which another entry holds a block is refused: evicting would
  *   change cells of the other row.

@@ -13,6 +13,12 @@ namespace {
 
 size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
 
+// Whether two arrays of ints have an entry in common.
+bool overlap(const int* a, int na, const int* b, int nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)nb * sizeof(int) && y < x + (uintptr_t)na * sizeof(int);
+}
+
 // Bytes of the decode kernel's partials and of the items' offsets in its tile list.
 size_t partial_bytes(const kvq_config& c, int batch, int workers) {
   const size_t items = (size_t)batch * c.num_kv_heads, slots = items + (size_t)workers;
@@ -102,7 +108,7 @@ kvq_status plan_shared(const kvq_ctx* ctx, int layer, int batch, int num_groups,
   if (st != KVQ_OK) return st;
   if (ctx->window[layer] != 0) return KVQ_ERR_UNSUPPORTED;
   if (batch < 0 || num_groups < 0 || max_group < 0 || max_shared < 0 || max_own < 0 ||
-      max_shared > (1 << 30) || max_own > (1 << 30) || num_splits < 0 || num_splits > 1024)
+      max_shared >= (1 << 30) || max_own >= (1 << 30) || num_splits < 0 || num_splits > 1024)
     return KVQ_ERR_INVALID_ARG;
   const kvq_config& c = ctx->cfg;
   if (max_group > batch) max_group = batch;
@@ -358,6 +364,11 @@ kvq_status kvq_evict_cells(const kvq_ctx* ctx, int layer, const int* rows, const
   const int cluster = evict_cluster(max_context, items);
   if (cluster == 0) return KVQ_ERR_UNSUPPORTED;
   if (items * cluster >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
+  // written while other CTAs of the row still read these
+  if (overlap(new_lens, num_rows, context_lens, table_rows) ||
+      overlap(new_lens, num_rows, rows, num_rows) ||
+      (keep_lens != new_lens && overlap(new_lens, num_rows, keep_lens, num_rows)))
+    return KVQ_ERR_INVALID_ARG;
   unsigned* err = error_word();
   if (!err) return KVQ_ERR_CUDA;
   EvictArgs a = {};

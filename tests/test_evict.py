@@ -57,6 +57,16 @@ def test_refuses(match, kw):
         _call(**kw)
 
 
+@pytest.mark.parametrize("kw", [
+    dict(new=OK), dict(new=OK + 8), dict(new=OK - 4, n=2), dict(new=OK + 0x1000), dict(new=OK + 0x1004, n=2),
+    dict(new=OK + 0xffc), dict(new=OK + 0x2004), dict(new=OK + 0x1ffc),
+])
+def test_lengths_are_not_written_over_what_the_call_reads(kw):
+    """3 lengths at OK, 2 rows at OK + 0x1000, 2 budgets at OK + 0x2000."""
+    with pytest.raises(kvq.KVQError, match="INVALID_ARG"):
+        _call(rows=OK + 0x1000, keep=OK + 0x2000, table=OK + 0x3000, **kw)
+
+
 def test_nothing_to_do():
     _call(n=0)
 

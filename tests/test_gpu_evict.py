@@ -204,3 +204,18 @@ def test_stream_and_graph():
     for x, y in zip(c.bufs + [c.weights], got):
         assert torch.equal(x, y)
     assert new.tolist() == [150, 120]
+
+
+def test_new_lengths_over_the_budgets():
+    """keep_lens is new_lens: the same moves, rows that are refused among them."""
+    lens = [3000, 100, 5000, 90, 120]
+    rows, keeps = [0, 1, -1, 2, 3, 4], [2000, 50, 7, 3000, 100, 11]
+    c, d = Case(lens, seed=18), Case(lens, seed=18)
+    c.run(rows, keeps, 4, 8)
+    over = _i32(keeps)
+    d.call(_i32(rows), over, over, 4, 8, d.most, None)
+    torch.cuda.synchronize()
+    assert K().kvq_get_device_error() == BAD
+    assert over.tolist() == [2000, 50, 0, 3000, 90, 120]
+    for x, y in zip(c.bufs + [c.weights], d.bufs + [d.weights]):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))

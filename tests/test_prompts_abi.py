@@ -36,6 +36,7 @@ def test_shared_plan():
     ("INVALID_ARG", dict(layer=2)), ("INVALID_ARG", dict(batch=-1)), ("INVALID_ARG", dict(groups=-1)),
     ("INVALID_ARG", dict(max_group=-1)), ("INVALID_ARG", dict(max_shared=-1)), ("INVALID_ARG", dict(max_own=-1)),
     ("INVALID_ARG", dict(max_shared=(1 << 30) + 1)), ("INVALID_ARG", dict(max_own=(1 << 30) + 1)),
+    ("INVALID_ARG", dict(max_shared=1 << 30, max_own=1 << 30)),
     ("INVALID_ARG", dict(splits=-1)), ("INVALID_ARG", dict(splits=1025)),
     ("INVALID_ARG", dict(groups=(1 << 31) - 1, batch=(1 << 31) - 1, max_group=(1 << 31) - 1)),
     ("INVALID_ARG", dict(groups=1 << 20, batch=1 << 20, max_group=1 << 20)),
