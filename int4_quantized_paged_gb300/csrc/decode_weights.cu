@@ -32,7 +32,11 @@ __global__ void __launch_bounds__(AT)
   const int b = blockIdx.z, g = blockIdx.y;
   const int L = ctx_len(a, b);
   const int p0 = blockIdx.x * (AT * AU) + threadIdx.x;
-  if ((int)blockIdx.x * (AT * AU) >= L) return;
+  if ((int)blockIdx.x * (AT * AU) >= L) {
+    // this grid does not end before the one it was launched behind, even if no row has a cell
+    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   float* row = weights + ((long long)b * a.Hkv + g) * stride;
   float past[AU];
 #pragma unroll
