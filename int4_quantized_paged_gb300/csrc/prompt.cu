@@ -58,6 +58,7 @@
 
 #include "async_copy.cuh"
 #include "kvq_internal.h"
+#include "prompt_items.h"
 #include "tcgen05.cuh"
 #include "tile_math.cuh"
 
@@ -106,10 +107,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// What a CTA works on: positions [p0, end) of the sequence that starts at token t0,
-// KV head g; p0 < 0: nothing is left.
-struct Item {
-  int t0, p0, end, g;
+using Item = PromptItem;                       // what a CTA works on
+
+// 32 sequences at a time, one for each lane; the first ones' lengths are kept.
+struct WarpLanes {
+  const PromptSeqs& s;
+  int lane, first;
+
+  __device__ __forceinline__ unsigned longer(int b0, int than) const {
+    bool ignored = false;
+    return __ballot_sync(0xffffffffu, (b0 == 0 ? first : prompt_length(s, b0 + lane, &ignored)) > than);
+  }
+  __device__ __forceinline__ int nth(unsigned m, int r) const {
+    const bool me = ((m >> lane) & 1u) && __popc(m & ((1u << lane) - 1u)) == r;
+    return __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+  }
 };
 
 // Asks for the launch of one more CTA to be cancelled in favour of this one: 16 bytes
@@ -172,47 +184,9 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
   const int QP = ROWS >> a.g_shift;                        // positions per query tile
   const int per = NQ * QP;                                 // and per item
 
-  // ---- the producer's view of the sequences: item w of the list, by levels.  Level q
-  // has an item for each KV head of each sequence that is longer than q * per.
-  auto length = [&](int b) -> int {
-    if (b >= a.B) return 0;
-    const int t = a.seq_start[b], n = a.seq_start[b + 1] - t;
-    const bool bad = t < 0 || n < 0 || (long long)t + n > a.T;
-    if (blockIdx.x == 0 && (bad || n > a.max_len)) atomicOr(a.err, ERR_BAD_INDEX);
-    return bad ? 0 : min(n, a.max_len);                    // tokens past the caller's bound
-  };
-  int n0 = 0, level = 0, at_level = 0;                     // lengths of the first 32; level, its sequences
-  long long before = 0;                                    // items of the levels above
-  auto longer = [&](int b0, int than) -> unsigned {        // sequences b0 + bit
-    const int n = b0 == 0 ? n0 : length(b0 + lane);
-    return __ballot_sync(0xffffffffu, n > than);
-  };
-  auto find = [&](long long w) -> Item {
-    Item it = {0, -1, 0, 0};
-    while (w >= before + (long long)at_level * a.Hkv) {
-      before += (long long)at_level * a.Hkv;
-      if (--level < 0) return it;
-      at_level = 0;
-      for (int b0 = 0; b0 < a.B; b0 += 32) at_level += __popc(longer(b0, level * per));
-    }
-    int r = (int)(w - before) / a.Hkv;                     // which of the level's sequences
-    it.g = (int)(w - before) - r * a.Hkv;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const unsigned m = longer(b0, level * per);
-      const int here = __popc(m);
-      if (r < here) {
-        const bool me = ((m >> lane) & 1u) && __popc(m & ((1u << lane) - 1u)) == r;
-        const int b = b0 + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
-        it.t0 = a.seq_start[b];
-        it.p0 = level * per;
-        it.end = min(min(a.seq_start[b + 1] - it.t0, a.max_len), it.p0 + per);
-        return it;
-      }
-      r -= here;
-    }
-    return it;
-  };
-
+  const PromptSeqs seqs = {a.seq_start, a.T, a.B, a.max_len, a.Hkv, per};
+  WarpLanes lanes = {seqs, lane, 0};
+  int longest = 0;
   Item first = {0, -1, 0, 0};
   if (warp == C::PROD) {
     if (elect_one()) {
@@ -220,12 +194,16 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
       prefetch_map(&kmap);
       prefetch_map(&vmap);
     }
-    n0 = length(lane);
-    int most = n0;
-    for (int b0 = 32; b0 < a.B; b0 += 32) most = max(most, length(b0 + lane));
-    most = __reduce_max_sync(0xffffffffu, most);
-    level = (most + per - 1) / per;
-    first = find(blockIdx.x);
+    bool wrong = false;
+    longest = lanes.first = prompt_length(seqs, lane, &wrong);
+    for (int b0 = 32; b0 < a.B; b0 += 32) longest = max(longest, prompt_length(seqs, b0 + lane, &wrong));
+    // every CTA that starts tells: which ones do is not known
+    if (wrong) atomicOr(a.err, ERR_BAD_INDEX);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+  }
+  PromptSearch<WarpLanes> items_of_call(seqs, lanes, longest);   // the producer's
+  if (warp == C::PROD) {
+    first = items_of_call.find(blockIdx.x);
     if (lane == 0) *s_abort = first.p0 < 0;
   }
   if (tid == 0) {
@@ -373,7 +351,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
         fence_proxy_async();                               // read before it is written again
         __syncwarp();
         it.p0 = -1;
-        if (w >= 0) it = find(w);
+        if (w >= 0) it = items_of_call.find(w);
         ++k;
       }
       // every copy has landed before the CTA exits
