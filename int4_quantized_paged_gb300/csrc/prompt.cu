@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
   const PromptSeqs seqs = {a.seq_start, a.T, a.B, a.max_len, a.Hkv, per};
   WarpLanes lanes = {seqs, lane, 0};
   int longest = 0;
+  bool descends = false;                                   // starts do: sequences may overlap
   Item first = {0, -1, 0, 0};
   if (warp == C::PROD) {
     if (elect_one()) {
@@ -195,8 +196,13 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
       prefetch_map(&vmap);
     }
     bool wrong = false;
-    longest = lanes.first = prompt_length(seqs, lane, &wrong);
-    for (int b0 = 32; b0 < a.B; b0 += 32) longest = max(longest, prompt_length(seqs, b0 + lane, &wrong));
+    auto look = [&](int b) -> int {
+      descends |= b < a.B && a.seq_start[b + 1] < a.seq_start[b];
+      return prompt_length(seqs, b, &wrong);
+    };
+    longest = lanes.first = look(lane);
+    for (int b0 = 32; b0 < a.B; b0 += 32) longest = max(longest, look(b0 + lane));
+    descends = __any_sync(0xffffffffu, descends);
     // every CTA that starts tells: which ones do is not known
     if (wrong) atomicOr(a.err, ERR_BAD_INDEX);
     longest = __reduce_max_sync(0xffffffffu, longest);
@@ -303,6 +309,8 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
         return true;
       };
       int loaded = 0;                                      // items whose Q was loaded
+      int asks = 0;                                        // answers waited for
+      long long w = blockIdx.x;                            // the item's number
       for (bool go = publish(); go && it.p0 >= 0; go = publish()) {
         const int nqt = query_tiles(it), kt0 = first_tile(it), ntl = tiles_of(it, nqt - 1);
         if constexpr (C::QTM) {
@@ -336,22 +344,38 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
           __syncwarp();
           ++loaded;
         }
+        // Sequences that overlap can have more items than the grid has CTAs; number w then
+        // goes on as w + grid
+        Item behind = {0, -1, 0, 0};
+        bool waiting = false;                              // for an answer
         for (int i = 0; go && i < ntl; ++i) {
-          if (i == max(0, ntl - 2) && elect_one()) {       // the next item, no earlier than needed
-            mbar_expect_tx(asked, 16);
-            ask_for_item(answer, asked);
+          if (i == max(0, ntl - 2)) {                      // the next item, no earlier than needed
+            if (descends) behind = items_of_call.find(w + gridDim.x);
+            if (behind.p0 < 0) {
+              if (elect_one()) {
+                mbar_expect_tx(asked, 16);
+                ask_for_item(answer, asked);
+              }
+              waiting = true;
+            }
           }
           __syncwarp();
           go = load(&vmap, (kt0 + i) * KT);
           if (go && i + SB < ntl) go = load(&kmap, (kt0 + i + SB) * KT);
         }
         // the answer arrives in any case (and has to, before the CTA exits)
-        if (!wait(asked, (uint32_t)(k & 1)) || !go) break;
-        const long long w = read_answer(answer);
-        fence_proxy_async();                               // read before it is written again
-        __syncwarp();
-        it.p0 = -1;
-        if (w >= 0) it = items_of_call.find(w);
+        if (waiting && !wait(asked, (uint32_t)(asks++ & 1))) break;
+        if (!go) break;
+        if (waiting) {
+          w = read_answer(answer);
+          fence_proxy_async();                             // read before it is written again
+          __syncwarp();
+          it.p0 = -1;
+          if (w >= 0) it = items_of_call.find(w);
+        } else {
+          it = behind;
+          w += gridDim.x;
+        }
         ++k;
       }
       // every copy has landed before the CTA exits
