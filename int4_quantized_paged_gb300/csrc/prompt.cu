@@ -22,14 +22,16 @@
 //  * producer warp: finds the items among the ragged sequences, loads Q, then K and V
 //    tiles by TMA straight into their operand layouts (rows of 128 bytes, 128-byte
 //    swizzle) through one ring of slots;
-//  * MMA warp, one elected lane: S_j = Q_j K^T into tensor memory and O_j += P_j V
-//    with P_j read from tensor memory, where it replaces S_j.  With two query tiles
-//    the order is PV_0, S_0, PV_1, S_1, so that the tensor cores work on one tile
+//  * two MMA warps, one elected lane each: one for S_j = Q_j K^T into tensor memory, one for
+//    O_j += P_j V with P_j read from tensor memory, where it replaces S_j.  With two query
+//    tiles PV_0, S_0, PV_1, S_1 follow one another, so that the tensor cores work on one tile
 //    during the other's softmax; with one (head_dim 256, whose O takes half of
 //    tensor memory) S has two buffers and runs a key tile ahead;
 //  * a softmax warpgroup per query tile, one thread per row (its tensor-memory lane).
-// A CTA's MMAs run in the order of their issue, so S_j(i + 1) may be issued behind
-// the PV_j(i) that still reads P from the same columns.
+// MMAs with different accumulators may run in any order.  S_j(i + SB) overwrites the
+// columns that PV_j(i) reads, so it is issued when that one has completed.  That is what
+// S has a warp of its own for: one warp that waited between the two held back the other
+// query tile's PV as well (16,384 tokens: 1,650 us; two warps 1,390-1,410).
 //
 // Nothing beyond an item's last position is multiplied: the last key tile's MMAs
 // stop at the 16 keys that hold it, and the V rows between it and their end are set
@@ -38,19 +40,19 @@
 // Every wait is bounded; one that runs out flags TIMEOUT and ends every role.
 //
 // What bounds it, and measured.  Long prompts: the tensor cores, which the softmax threads
-// feed: 16,384 tokens, 32 heads of 128: 1,400 us, 1,560 TFLOP/s (0.83 of the cuBLAS bf16
-// rate); 8 sequences of 500-4,096: 234 us, 1,340.  A key tile pair takes about 3,000
+// feed: 16,384 tokens, 32 heads of 128: 1,400 us, 1,570 TFLOP/s (0.84 of the cuBLAS bf16
+// rate); 8 sequences of 500-4,096: 238 us, 1,320.  A key tile pair takes about 3,000
 // cycles, of which the MMAs are 2,048 at their peak rate and a softmax warp's own part
-// 1,230 (max 410, exponents and sums 750).  head_dim 256: 210 us, 1,260 TFLOP/s on 3
+// 1,230 (max 410, exponents and sums 750).  head_dim 256: 194 us, 1,360 TFLOP/s on 3
 // sequences of 1,500-4,000; 64: the softmax (as many exponents for half of the flops),
-// 950 TFLOP/s on 8,192 tokens, 64 heads.  Windows and short sequences: an item's chain
+// 960 TFLOP/s on 8,192 tokens, 64 heads.  Windows and short sequences: an item's chain
 // of barriers and its epilogue, two or three key tiles long (window 128, 4 sequences of
-// 3,000-4,096, 64 heads of 64: 121 us; 48 of 1-120 tokens: 19 us).
+// 3,000-4,096, 64 heads of 64: 128 us; 48 of 1-120 tokens: 19 us).
 // Measured no faster: the maximum found beside exponents taken against the old
 // reference; 64 keys a tile with four query tiles (head_dim 64: 580 -> 817 us on the
 // long prompt, 120 -> 104 in the window); P in columns of its own, so that the next
-// scores need not wait for PV (head_dim 64: 579 -> 591 us); whole rows written by the
-// copy engine (121 -> 127 us in the window).
+// scores need not wait for PV (head_dim 64: 572 -> 618 us, 128 -> 139 in the window); whole
+// rows written by the copy engine (121 -> 127 us in the window).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -89,7 +91,7 @@ struct Shape {
   static constexpr int LIMIT = 232448 - 1024 - AUX - OUT;  // shared memory, less alignment
   static constexpr int NS = (LIMIT - QSM) / SLOT < 8 ? (LIMIT - QSM) / SLOT : 8;
   static constexpr int SMEM = QSM + NS * SLOT + OUT + AUX + 1024;
-  static constexpr int PROD = SOFT, MMA = SOFT + 1;
+  static constexpr int PROD = SOFT, MMA_S = SOFT + 1, MMA_PV = SOFT + 2;
   static constexpr int THREADS = (SOFT + 4) * 32;
   __host__ __device__ static constexpr int scol(int j, int b) { return NQ == 2 ? 128 * j : 256 + KT * b; }
   __host__ __device__ static constexpr int ocol(int j) { return NQ == 2 ? 256 + D * j : 0; }
@@ -171,13 +173,13 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
   uint64_t* q_empty = q_full + 1;                          // MMA (commit) -> producer
   uint64_t* s_full = q_empty + 1;                          // [NQ][SB] MMA (commit) -> softmax
   uint64_t* p_full = s_full + NQ * SB;                     // [NQ][SB] softmax -> MMA
-  uint64_t* pv_done = p_full + NQ * SB;                    // [NQ][SB] MMA (commit) -> softmax
+  uint64_t* pv_done = p_full + NQ * SB;                    // [NQ][SB] MMA (commit) -> MMA of S, softmax
   uint64_t* o_full = pv_done + NQ * SB;                    // [NQ] MMA (commit), an item's last PV
   uint64_t* o_empty = o_full + NQ;                         // [NQ] softmax -> MMA
-  uint64_t* fin = o_empty + NQ;                            // the MMA warp's own end
-  static_assert(48 + (2 * NS + 8 + 3 * NQ * SB + 2 * NQ + 2) * 8 <= C::AUX, "barriers");
-  volatile int* s_abort = reinterpret_cast<volatile int*>(fin + 1);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(fin + 1) + 1;
+  uint64_t* fin = o_empty + NQ;                            // [2] the MMA warps' own ends
+  static_assert(48 + (2 * NS + 8 + 3 * NQ * SB + 2 * NQ + 3) * 8 <= C::AUX, "barriers");
+  volatile int* s_abort = reinterpret_cast<volatile int*>(fin + 2);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(fin + 2) + 1;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
     mbar_init(asked, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&item_full[s], 1);
-      mbar_init(&item_empty[s], C::SOFT + 1);
+      mbar_init(&item_empty[s], C::SOFT + 2);
     }
     mbar_init(q_full, C::QTM ? 128 : 1);
     mbar_init(q_empty, 1);
@@ -233,7 +235,8 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
       mbar_init(&o_full[j], 1);
       mbar_init(&o_empty[j], 4);
     }
-    mbar_init(fin, 1);
+    mbar_init(&fin[0], 1);
+    mbar_init(&fin[1], 1);
     mbar_init_fence();
   }
   __syncthreads();
@@ -382,19 +385,15 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
       if (loaded > 0) (void)mbar_wait(q_full, (uint32_t)((loaded - 1) & 1));
       for (int x = max(0, issued - NS); x < issued; ++x)
         (void)mbar_wait(&full[x % NS], (uint32_t)((x / NS) & 1));
-    } else if (warp == C::MMA) {
-      // ---- MMA issuer
+    } else if (warp == C::MMA_S || warp == C::MMA_PV) {
+      // ---- MMA issuers: one for S, one for O
+      const bool scores = warp == C::MMA_S;
       const uint64_t dq = sw128_desc(qsm), dk = sw128_desc(ring), dv = sw128_mn_desc(ring, KT * 128);
-      int x = 0;                                           // next entry of the ring
+      int x = 0;                                           // the item's first entry in the ring
       int used[NQ], items_of[NQ];                          // query tile j's key tiles and items so far
 #pragma unroll
       for (int j = 0; j < NQ; ++j) used[j] = items_of[j] = 0;
-      auto take = [&](int& slot) -> bool {
-        slot = x % NS;
-        const bool ok = wait(&full[slot], (uint32_t)((x / NS) & 1));
-        ++x;
-        return ok;
-      };
+      auto take = [&](int entry) -> bool { return wait(&full[entry % NS], (uint32_t)((entry / NS) & 1)); };
       auto commit = [&](uint64_t* bar) {
         if (elect_one()) umma_commit(bar);
         __syncwarp();
@@ -410,102 +409,96 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
           nt[j] = j < nqt ? tiles_of(it, j) : 0;
           rest[j] = min(KT, (tile_end(it, j) - (kt0 + nt[j] - 1) * KT + 15) & ~15);
         }
-        auto issue_s = [&](int j, int i, int slot) {
-          const uint64_t qa = dq + (uint64_t)(j * (C::QB >> 4));
-          const uint64_t kb = dk + (uint64_t)(slot * (C::SLOT >> 4));
-          const int sb = (used[j] + i) % SB;
-          const uint32_t td = tmem + C::scol(j, sb);
-          const uint32_t id = mma_idesc<true>(ROWS, i == nt[j] - 1 ? rest[j] : KT);
-          if (elect_one()) {
-            tc_fence_after();
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-              const uint64_t b = kb + (uint64_t)((((s >> 2) * (KT * 128)) + (s & 3) * 32) >> 4);
-              if constexpr (C::QTM) umma_tmem_a(td, tmem + C::QCOL + 8 * s, b, id, s > 0);
-              else umma(td, qa + (uint64_t)((((s >> 2) * (ROWS * 128)) + (s & 3) * 32) >> 4), b, id, s > 0);
+        if (scores) {
+          go = wait(q_full, (uint32_t)(k & 1));
+          if constexpr (C::QTM) {                          // its slots have been read
+            if (lane == 0) {
+              mbar_arrive(&empty[x % NS]);
+              mbar_arrive(&empty[(x + 1) % NS]);
             }
-            umma_commit(&s_full[j * SB + sb]);
-          }
-          __syncwarp();
-        };
-        auto issue_pv = [&](int j, int i, int slot) {
-          const uint64_t vb = dv + (uint64_t)(slot * (C::SLOT >> 4));
-          const int sb = (used[j] + i) % SB;
-          const uint32_t td = tmem + C::ocol(j), ta = tmem + C::scol(j, sb);
-          const bool last = i == nt[j] - 1;
-          constexpr uint32_t id = mma_idesc<true>(ROWS, D) | MMA_B_MN_MAJOR;
-          if (elect_one()) {
-            tc_fence_after();
-            if (last) {
-              for (int s = 0; s < rest[j] / 16; ++s)
-                umma_tmem_a(td, ta + 8 * s, vb + (uint64_t)(s * (16 * 128 >> 4)), id, i > 0 || s > 0);
-            } else {
-#pragma unroll
-              for (int s = 0; s < KT / 16; ++s)
-                umma_tmem_a(td, ta + 8 * s, vb + (uint64_t)(s * (16 * 128 >> 4)), id, i > 0 || s > 0);
-            }
-            if constexpr (SB > 1) umma_commit(&pv_done[j * SB + sb]);
-            if (last) umma_commit(&o_full[j]);
-          }
-          __syncwarp();
-        };
-        go = wait(q_full, (uint32_t)(k & 1));
-        if constexpr (C::QTM) {                            // its slots have been read
-          if (lane == 0) {
-            mbar_arrive(&empty[x % NS]);
-            mbar_arrive(&empty[(x + 1) % NS]);
-          }
-          __syncwarp();
-          x += 2;
-        }
-        int slot = 0;
-        for (int i = 0; go && i < SB && i < ntl; ++i) {
-          go = take(slot);
-          if (!go) break;
-#pragma unroll
-          for (int j = 0; j < NQ; ++j)
-            if (i < nt[j]) issue_s(j, i, slot);
-          commit(&empty[slot]);
-        }
-        if (go && ntl <= SB) commit(q_empty);
-        for (int i = 0; go && i < ntl; ++i) {
-          int vslot = 0, kslot = 0;
-          go = take(vslot);
-          if (!go) break;
-          if (i == ntl - 1) {
-            // rows between the item's last position and the end of its 16 keys
-            const int from = it.end - (kt0 + i) * KT, to = (from + 15) & ~15;
-            uint8_t* v = ring + vslot * C::SLOT;
-            for (int e = lane; e < (to - from) * (D / 8); e += 32) {
-              const int row = from + e / (D / 8), c = e % (D / 8);
-              *reinterpret_cast<uint4*>(v + (c >> 3) * (KT * 128) + row * 128 + ((c & 7) << 4)) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async();
             __syncwarp();
+            x += 2;
           }
-          const bool more = i + SB < ntl;
-          bool have_k = false;
+          for (int i = 0; go && i < ntl; ++i) {
+            const int entry = x + (i < SB ? i : 2 * i + 1 - SB), slot = entry % NS;
+            go = take(entry);
 #pragma unroll
-          for (int j = 0; j < NQ; ++j) {
-            if (!go || i >= nt[j]) continue;
-            const int u = used[j] + i;
-            // O_j of the item before has been read
-            if (i == 0 && items_of[j] > 0) go = wait(&o_empty[j], (uint32_t)((items_of[j] - 1) & 1));
-            if (go) go = wait(&p_full[j * SB + u % SB], (uint32_t)((u / SB) & 1));
-            if (!go) continue;
-            issue_pv(j, i, vslot);
-            if (i + SB < nt[j]) {
-              if (!have_k) go = take(kslot);
-              have_k = true;
-              if (go) issue_s(j, i + SB, kslot);
+            for (int j = 0; j < NQ; ++j) {
+              if (!go || i >= nt[j]) continue;
+              const int u = used[j] + i, sb = u % SB;
+              // the PV whose P it replaces, perhaps of the item before, has read it
+              if (u >= SB) go = wait(&pv_done[j * SB + sb], (uint32_t)((u / SB - 1) & 1));
+              if (!go) continue;
+              const uint64_t qa = dq + (uint64_t)(j * (C::QB >> 4));
+              const uint64_t kb = dk + (uint64_t)(slot * (C::SLOT >> 4));
+              const uint32_t td = tmem + C::scol(j, sb);
+              const uint32_t id = mma_idesc<true>(ROWS, i == nt[j] - 1 ? rest[j] : KT);
+              if (elect_one()) {
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                  const uint64_t b = kb + (uint64_t)((((s >> 2) * (KT * 128)) + (s & 3) * 32) >> 4);
+                  if constexpr (C::QTM) umma_tmem_a(td, tmem + C::QCOL + 8 * s, b, id, s > 0);
+                  else umma(td, qa + (uint64_t)((((s >> 2) * (ROWS * 128)) + (s & 3) * 32) >> 4), b, id, s > 0);
+                }
+                umma_commit(&s_full[j * SB + sb]);
+              }
+              __syncwarp();
             }
+            if (go) commit(&empty[slot]);
           }
-          if (!go) break;
-          commit(&empty[vslot]);
-          if (more) commit(&empty[kslot]);
-          if (i + SB == ntl - 1) commit(q_empty);          // the item's last scores
+          if constexpr (!C::QTM) {
+            if (go) commit(q_empty);                       // behind the item's last scores
+          }
+        } else {
+          if constexpr (C::QTM) x += 2;
+          for (int i = 0; go && i < ntl; ++i) {
+            const int entry = x + min(SB, ntl) + i + min(i, max(ntl - SB, 0)), slot = entry % NS;
+            go = take(entry);
+            if (!go) break;
+            if (i == ntl - 1) {
+              // rows between the item's last position and the end of its 16 keys
+              const int from = it.end - (kt0 + i) * KT, to = (from + 15) & ~15;
+              uint8_t* v = ring + slot * C::SLOT;
+              for (int e = lane; e < (to - from) * (D / 8); e += 32) {
+                const int row = from + e / (D / 8), c = e % (D / 8);
+                *reinterpret_cast<uint4*>(v + (c >> 3) * (KT * 128) + row * 128 + ((c & 7) << 4)) =
+                    make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+              if (!go || i >= nt[j]) continue;
+              const int u = used[j] + i, sb = u % SB;
+              // O_j of the item before has been read
+              if (i == 0 && items_of[j] > 0) go = wait(&o_empty[j], (uint32_t)((items_of[j] - 1) & 1));
+              if (go) go = wait(&p_full[j * SB + sb], (uint32_t)((u / SB) & 1));
+              if (!go) continue;
+              const uint64_t vb = dv + (uint64_t)(slot * (C::SLOT >> 4));
+              const uint32_t td = tmem + C::ocol(j), ta = tmem + C::scol(j, sb);
+              const bool last = i == nt[j] - 1;
+              constexpr uint32_t id = mma_idesc<true>(ROWS, D) | MMA_B_MN_MAJOR;
+              if (elect_one()) {
+                tc_fence_after();
+                if (last) {
+                  for (int s = 0; s < rest[j] / 16; ++s)
+                    umma_tmem_a(td, ta + 8 * s, vb + (uint64_t)(s * (16 * 128 >> 4)), id, i > 0 || s > 0);
+                } else {
+#pragma unroll
+                  for (int s = 0; s < KT / 16; ++s)
+                    umma_tmem_a(td, ta + 8 * s, vb + (uint64_t)(s * (16 * 128 >> 4)), id, i > 0 || s > 0);
+                }
+                umma_commit(&pv_done[j * SB + sb]);
+                if (last) umma_commit(&o_full[j]);
+              }
+              __syncwarp();
+            }
+            if (go) commit(&empty[slot]);
+          }
         }
+        x += 2 * ntl;
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
           used[j] += nt[j];
@@ -513,8 +506,8 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
         }
       }
       // what was issued completes before the CTA exits
-      commit(fin);
-      (void)mbar_wait(fin, 0u);
+      commit(&fin[scores]);
+      (void)mbar_wait(&fin[scores], 0u);
     }
   } else {
     if constexpr (C::MOVE_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
@@ -620,7 +613,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
         }
         l *= al;
         if (i > 0 && __any_sync(0xffffffffu, al != 1.f)) {
-          // with one S buffer S(i) ran behind PV(i - 1), which is then done
+          // with one S buffer S(i) was issued when PV(i - 1) was done
           if constexpr (SB > 1) {
             ok = wait(&pv_done[j * SB + (u - 1) % SB], (uint32_t)(((u - 1) / SB) & 1));
             if (!ok) break;
