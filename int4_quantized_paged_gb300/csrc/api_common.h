@@ -57,17 +57,4 @@ inline PageTables page_tables(const kvq_ctx* ctx, int* ref_count, int* block_tab
   return t;
 }
 
-inline kvq_status check_tables(const kvq_ctx* ctx, const int* ref_count, const int* block_table,
-                               int rows, int max_blocks, const int* context_lens) {
-  if (!ctx || rows < 0 || max_blocks < 0) return KVQ_ERR_INVALID_ARG;
-  if ((long long)max_blocks * ctx->cfg.block_size >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
-  if (!ref_count || !block_table || !context_lens) return KVQ_ERR_INVALID_ARG;
-  if (!aligned4(ref_count) || !aligned4(block_table) || !aligned4(context_lens))
-    return KVQ_ERR_ALIGNMENT;
-  return KVQ_OK;
-}
-
-// Splits of the keys of an attention without a mask (api_serving.cu).
-int plan_splits(long long base, int tiles);
-
 }  // namespace kvq

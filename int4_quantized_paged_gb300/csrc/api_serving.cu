@@ -21,28 +21,6 @@ struct kvq_rope {
 
 using namespace kvq;
 
-// Splits of the keys for `base` CTAs (query tiles x sequences x KV heads) over
-// `tiles` key tiles: the count whose waves over the SMs take the least time, in
-// units of a key tile (about 1 us): a CTA costs its tiles and about three more
-// for its queries, barriers and epilogue; joining splits costs about three and
-// a little per split.
-int kvq::plan_splits(long long base, int tiles) {
-  const int sms = sm_count();
-  int best = 1;
-  double best_cost = 1e300;
-  for (int s = 1; s <= tiles && s <= 128; ++s) {
-    const int per = (tiles + s - 1) / s;
-    if (s > 1 && (tiles + per - 1) / per != s) continue;     // fewer splits do the same
-    const double waves = (double)((base * s + sms - 1) / sms);
-    const double cost = waves * (per + 3.0) + (s > 1 ? 3.0 + 0.05 * s : 0.0);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = s;
-    }
-  }
-  return best;
-}
-
 namespace {
 
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
@@ -58,6 +36,38 @@ unsigned long long turn_fraction(double f) {
   double turns = f / kTwoPi;
   turns -= floor(turns);
   return turns >= 1.0 ? 0ull : (unsigned long long)ldexp(turns, 64);
+}
+
+kvq_status check_tables(const kvq_ctx* ctx, const int* ref_count, const int* block_table, int rows,
+                        int max_blocks, const int* context_lens) {
+  if (!ctx || rows < 0 || max_blocks < 0) return KVQ_ERR_INVALID_ARG;
+  if ((long long)max_blocks * ctx->cfg.block_size >= (1LL << 31)) return KVQ_ERR_INVALID_ARG;
+  if (!ref_count || !block_table || !context_lens) return KVQ_ERR_INVALID_ARG;
+  if (!aligned4(ref_count) || !aligned4(block_table) || !aligned4(context_lens))
+    return KVQ_ERR_ALIGNMENT;
+  return KVQ_OK;
+}
+
+// Splits of the keys for `base` CTAs (query tiles x sequences x KV heads) over
+// `tiles` key tiles: the count whose waves over the SMs take the least time, in
+// units of a key tile (about 1 us): a CTA costs its tiles and about three more
+// for its queries, barriers and epilogue; joining splits costs about three and
+// a little per split.
+int plan_splits(long long base, int tiles) {
+  const int sms = sm_count();
+  int best = 1;
+  double best_cost = 1e300;
+  for (int s = 1; s <= tiles && s <= 128; ++s) {
+    const int per = (tiles + s - 1) / s;
+    if (s > 1 && (tiles + per - 1) / per != s) continue;     // fewer splits do the same
+    const double waves = (double)((base * s + sms - 1) / sms);
+    const double cost = waves * (per + 3.0) + (s > 1 ? 3.0 + 0.05 * s : 0.0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
 // Splits (0 in: the plan's choice) and workspace bytes of a cross attention call

@@ -249,7 +249,7 @@ cudaError_t launch_prefix(int mode, int D, int G, const DecodeArgs& a, const Sha
   PrefillArgs pa = {};
   pa.d = a;
   pa.query_start = x.group_start;
-  pa.qtiles = 1;                               // not read: a unit names its query tile
+  pa.qtiles = 1;                               // divided by, then a unit names its query tile
   pa.g_shift = __builtin_ctz((unsigned)G);
   pa.max_query = x.max_group;
   pa.splits = x.max_units;                     // CTAs per KV head

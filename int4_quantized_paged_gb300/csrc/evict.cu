@@ -389,8 +389,8 @@ __global__ void __launch_bounds__(ET, 3) evict_kernel(const EvictArgs a) {
 
 }  // namespace
 
-// CTAs per (row, KV head): as many as fill the SMs about twice, with no fewer than
-// 1,024 cells each, and as many as hold the row's weights.  0: no cluster does.
+// CTAs per (row, KV head): as many as fill the SMs about twice, though no segment of 1,024
+// cells or fewer is cut, and as many as hold the row's weights.  0: no cluster does.
 int evict_cluster(int max_len, long long items) {
   int cs = 1;
   const long long sms = sm_count();
