@@ -565,7 +565,8 @@ kvq_status kvq_cross_plan(const kvq_ctx* ctx, int layer, int batch, int max_quer
  *   its row of out is then undefined.)
  * out: bf16 [num_tokens][Hq][D], 16-byte aligned; it overlaps none of q, k and v.
  * Scores, softmax statistics and sums are fp32; the weight that meets v, relative
- * to the row's largest (to within 2^8), is rounded to bf16, as the output is.
+ * to the row's largest (to within 2^8), is rounded to bf16, as the output is
+ * (kvq_prefill_attention keeps two f16 terms of it).
  * Values of a sequence that are not finite may reach any of its rows, and no row of
  * another sequence.  No workspace. */
 kvq_status kvq_prompt_attention(const kvq_ctx* ctx, int layer, const void* q,
@@ -583,7 +584,9 @@ kvq_status kvq_prompt_attention(const kvq_ctx* ctx, int layer, const void* q,
  * kvq_fork_sequences shares, or copies of them, as a row that grew has one of the
  * last, partly filled block.  They are read through the table row of the group's
  * first row.  A row attends to all of its context_lens[b] positions, those of the
- * prefix among them; a prefix longer than a row of the group is cut to that row.
+ * prefix among them; a prefix longer than a row of the group is cut to that row, for
+ * all rows of the group: one of length 0 (a padded batch) has the others read theirs
+ * each for itself, so such a row is better left out of the group.
  *
  * q: bf16 [batch][Hq][D]; out: bf16 [batch][Hq][D], both 16-byte aligned.  L = 0
  *   gives a zero row.
@@ -599,8 +602,10 @@ kvq_status kvq_prompt_attention(const kvq_ctx* ctx, int layer, const void* q,
  *   positions behind its prefix, for the plan only.
  * num_splits, workspace: as for kvq_shared_prefix_plan, with the same sizes.  The
  *   workspace (16-byte aligned) needs no initialisation; overlapping calls need one each.
- * Softmax and sums are fp32; over the prefix, the weight that meets a V code is
- * rounded as kvq_cross_attention says.  A layer with a window is
+ * Softmax and sums are fp32; over a prefix that is shared, the weight that meets a V
+ * code is rounded as kvq_cross_attention says, to fewer bits than kvq_decode_attention
+ * keeps.  Whether and in which splits it is shared goes by the lengths of the whole
+ * batch, so a row's last bits may change with the rows beside it.  A layer with a window is
  * KVQ_ERR_UNSUPPORTED (it reads no long prefix).  Starts that descend or leave
  * [0, batch] set KVQ_ERR_BAD_INDEX and nothing is shared; a negative shared length sets
  * it and its group shares nothing; lengths and block ids as kvq_decode_attention treats them.  Scale
@@ -639,8 +644,8 @@ kvq_status kvq_shared_prefix_plan(const kvq_ctx* ctx, int layer, int batch, int 
  *   start from 0: zero a row when its sequence begins (kvq_evict_cells does so for
  *   the places that it frees).  Rows must not overlap.
  * num_workers, workspace: from kvq_decode_weights_plan; the workspace (16-byte
- *   aligned, no initialisation) holds the scores, so it is needed with one worker
- *   too.  A layer with a window is KVQ_ERR_UNSUPPORTED.  batch <= 65535.
+ *   aligned, no initialisation) holds the scores, batch x Hq x max_context floats
+ *   whatever the lengths are, so it is needed with one worker too.  A layer with a window is KVQ_ERR_UNSUPPORTED.  batch <= 65535.
  * The sums do not depend on the order of atomics: the same call gives the same bits.
  * A weight is exact to a few times 2^-24 of itself and of the scores' size. */
 kvq_status kvq_decode_attention_weights(const kvq_ctx* ctx, int layer, const void* q,
@@ -670,7 +675,10 @@ kvq_status kvq_decode_weights_plan(const kvq_ctx* ctx, int layer, int batch, int
  *   - the last last_kept cells go, in order, to [keep - last_kept, keep).
  * Codes, dynamic scales and weights move together; weights[row][h][keep .. L) become
  * 0, and the codes and scales there stay what they were.  What a cell's position in
- * the sequence was (its rotation, a token's next position) does not change by this.
+ * the sequence was (its rotation, a token's next position) does not change by this, but
+ * kvq_extend_sequences counts from the length that the row then has: the positions that
+ * it writes are no longer the tokens' own.  A caller that evicts keeps each sequence's
+ * number of tokens and rotates by that.
  *
  * The call reads and writes one layer and changes no length and no table: after
  * the call for every layer of the pool, kvq_truncate_sequences(rows, new_lens) sets

@@ -47,7 +47,7 @@
 // sequences of 1,500-4,000; 64: the softmax (as many exponents for half of the flops),
 // 960 TFLOP/s on 8,192 tokens, 64 heads.  Windows and short sequences: an item's chain
 // of barriers and its epilogue, two or three key tiles long (window 128, 4 sequences of
-// 3,000-4,096, 64 heads of 64: 128 us; 48 of 1-120 tokens: 19 us).
+// 3,000-4,096, 64 heads of 64: 121-128 us; 48 of 1-120 tokens: 19.5 us).
 // Measured no faster: the maximum found beside exponents taken against the old
 // reference; 64 keys a tile with four query tiles (head_dim 64: 580 -> 817 us on the
 // long prompt, 120 -> 104 in the window); P in columns of its own, so that the next
